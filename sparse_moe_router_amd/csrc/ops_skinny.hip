@@ -1,0 +1,170 @@
+// y = x W^T for few rows an expert (gfx950, wave64): the decode and
+// small-batch form of the grouped and 8-bit products, bound by the stream of
+// the weights.
+//
+// A four-wave workgroup takes 16 rows of one expert's weights and all rows of
+// the expert's group, 16, 32 or 64 at a time.  The waves split the reduction,
+// each in runs of 512 bytes of every weight row, straight from global memory
+// into the MFMA operands (16x16 blocks: lane l holds 16 bytes of row l % 16),
+// eight weight loads in flight a wave; the four partial sums meet in LDS and
+// are added in wave order.  The weights are read once and, as such, with the
+// non-temporal hint; the few activation rows come from the caches.
+#include <type_traits>
+
+#include "ops_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int SN = 16;  // weight rows of a workgroup
+constexpr int SW = 4;   // waves
+constexpr int SUN = 8;  // 64-byte steps of a wave's run
+
+__device__ __align__(16) const uint32_t kZero[4] = {0, 0, 0, 0};
+
+struct SkinnyArgs {
+  Groups g;
+  const char* x;
+  const char* w;
+  Scales sc;
+  void* y;
+  int fp32;
+  int by_row;  // workgroup row = row of the grouped order (else the expert)
+};
+
+template <bool I8, int NB>
+__device__ __forceinline__ void skinny_block(const SkinnyArgs& p, int e, int n0, int64_t p0, int rows, float* red) {
+  typedef typename std::conditional<I8, i32x4_t, f32x4_t>::type acc_t;
+  constexpr int ES = I8 ? 1 : 2;
+  const Groups& g = p.g;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int KC = g.K * ES / 16;        // 16-byte chunks of a row
+  const int steps = (KC + 3) / 4;      // 64-byte steps
+  const int n = n0 + l16;
+  const char* wrow = p.w + ((int64_t)e * g.N + (n < g.N ? n : 0)) * g.K * ES + quad * 16;
+  const int wlim = n < g.N ? KC : 0;
+  const char* xrow[NB];
+  int xlim[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int r = 16 * b + l16;
+    const int64_t t = r < rows ? source_row(g, p0 + r) : -1;
+    xrow[b] = p.x + (t < 0 ? 0 : t) * g.ldx * ES + quad * 16;
+    xlim[b] = t < 0 ? 0 : KC;
+  }
+  acc_t acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = (acc_t){};
+  for (int s0 = SUN * wave; s0 < steps; s0 += SUN * SW) {
+    u32x4_t wf[SUN], xf[NB][SUN];
+#pragma unroll
+    for (int u = 0; u < SUN; ++u) {
+      const int c = 4 * (s0 + u) + quad;
+      wf[u] = __builtin_nontemporal_load((const u32x4_t*)(c < wlim ? wrow + (int64_t)(s0 + u) * 64 : (const char*)kZero));
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int u = 0; u < SUN; ++u) {
+        const int c = 4 * (s0 + u) + quad;
+        xf[b][u] = *(const u32x4_t*)(c < xlim[b] ? xrow[b] + (int64_t)(s0 + u) * 64 : (const char*)kZero);
+      }
+#pragma unroll
+    for (int u = 0; u < SUN; ++u)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if constexpr (I8)
+          acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, wf[u]),
+                                                         __builtin_bit_cast(i32x4_t, xf[b][u]), acc[b], 0, 0, 0);
+        else
+          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wf[u]),
+                                                           __builtin_bit_cast(bf16x8_t, xf[b][u]), acc[b], 0, 0, 0);
+      }
+  }
+  // block layout: lane -> x row l16, register r -> weight row 4 quad + r
+  typedef typename std::conditional<I8, int32_t, float>::type el_t;
+  el_t* rd = (el_t*)red;  // [wave][16 NB rows][16]
+#pragma unroll
+  for (int b = 0; b < NB; ++b) *(acc_t*)(rd + ((wave * 16 * NB) + 16 * b + l16) * 16 + 4 * quad) = acc[b];
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * 8; i += 64 * SW) {  // two weight rows a thread
+    const int r = i >> 3, c = 2 * (i & 7), col = n0 + c;
+    if (col >= g.N) continue;
+    el_t v0 = 0, v1 = 0;
+#pragma unroll
+    for (int w = 0; w < SW; ++w) {
+      v0 += rd[(w * 16 * NB + r) * 16 + c];
+      v1 += rd[(w * 16 * NB + r) * 16 + c + 1];
+    }
+    float f0 = (float)v0, f1 = (float)v1;
+    if (I8) {
+      const int64_t t = source_row(g, p0 + r);
+      const float xs = t < 0 ? 0.0f : p.sc.x[t];
+      const float* ws = p.sc.w + (int64_t)e * g.N + col;
+      f0 = f0 * (xs * ws[0]) + (p.sc.bias ? p.sc.bias[col] : 0.0f);
+      f1 = f1 * (xs * ws[1]) + (p.sc.bias ? p.sc.bias[col + 1] : 0.0f);
+    }
+    if (p.fp32) {
+      float* o = (float*)p.y + (p0 + r) * g.ldy + col;
+      o[0] = f0;
+      o[1] = f1;
+    } else {
+      *(uint32_t*)((uint16_t*)p.y + (p0 + r) * g.ldy + col) = pack_bf16x2(f0, f1);
+    }
+  }
+}
+
+template <bool I8>
+__global__ __launch_bounds__(64 * SW) void k_op_skinny(SkinnyArgs p) {
+  __shared__ float red[SW * 64 * 16];
+  const Groups& g = p.g;
+  const int n0 = blockIdx.x * SN;
+  int e = blockIdx.y;
+  if (p.by_row) {
+    // the expert of row blockIdx.y, taken by the workgroup of its first row
+    const int64_t row = blockIdx.y;
+    const int lane = threadIdx.x & 63;
+    e = 0;
+    for (int i = lane; i < (g.E + 63) / 64 * 64; i += 64)
+      e += __builtin_popcountll(__ballot(i < g.E && g.offsets[i + 1] <= row));
+    e = __builtin_amdgcn_readfirstlane(e);
+    if (e >= g.E) return;
+    int64_t lo, hi;
+    group_range(g, e, &lo, &hi);
+    if (lo != row) return;
+  }
+  int64_t lo, hi;
+  group_range(g, e, &lo, &hi);
+  while (lo < hi) {
+    const int rows = (int)(hi - lo < 64 ? hi - lo : 64);
+    if (rows <= 16)
+      skinny_block<I8, 1>(p, e, n0, lo, rows, red);
+    else if (rows <= 32)
+      skinny_block<I8, 2>(p, e, n0, lo, rows, red);
+    else
+      skinny_block<I8, 4>(p, e, n0, lo, rows, red);
+    lo += rows;
+    if (lo < hi) __syncthreads();  // the partial sums are read before they are overwritten
+  }
+}
+
+}  // namespace
+
+hipError_t launch_op_skinny(bool i8, const Groups& g, const void* x, const void* w, const Scales& sc, void* y,
+                            bool fp32, hipStream_t s) {
+  SkinnyArgs a{};
+  a.g = g;
+  a.x = (const char*)x;
+  a.w = (const char*)w;
+  a.sc = sc;
+  a.y = y;
+  a.fp32 = fp32;
+  a.by_row = g.offsets && g.rows < g.E;
+  const dim3 grid((unsigned)((g.N + SN - 1) / SN), (unsigned)(a.by_row ? g.rows : g.E));
+  const Launch lc{s, nullptr, nullptr};
+  if (i8) return launch(lc, k_op_skinny<true>, grid, dim3(64 * SW), a);
+  return launch(lc, k_op_skinny<false>, grid, dim3(64 * SW), a);
+}
+
+}  // namespace moe
