@@ -4,10 +4,12 @@
 
 produces ``sparse_moe_router_amd/libmoe_layer.so`` (the layer's C ABI and
 kernels), ``synth/libsynth.so`` (the device twin of the seeded input
-generator used by tests and the benchmark) and ``synth/libsynth_host.so``
-(its host twin in C, built with gcc) and
+generator used by tests and the benchmark), ``synth/libsynth_host.so``
+(its host twin in C, built with gcc),
 ``sparse_moe_router_amd/libmoe_peaks.so`` (the two measurement kernels of
-``include/moe_peaks.h``: sustainable HBM read and bf16 MFMA rates).
+``include/moe_peaks.h``: sustainable HBM read and bf16 MFMA rates) and
+``sparse_moe_router_amd/_ops.so`` (the Python module behind ``ops.py``, host
+code built with g++ against torch's headers).
 """
 from __future__ import annotations
 
@@ -34,6 +36,7 @@ LIB = os.path.join(PKG, "libmoe_layer.so")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libsynth.so")
 SYNTH_HOST_LIB = os.path.join(ROOT, "synth", "libsynth_host.so")
 PEAKS_LIB = os.path.join(PKG, "libmoe_peaks.so")
+OPS_MODULE = os.path.join(PKG, "_ops.so")
 
 
 def _run(cmd):
@@ -94,8 +97,25 @@ def build_peaks() -> str:
     return PEAKS_LIB
 
 
+def build_ops_module() -> str:
+    """The binding of the operators; links to the layer's library, found beside it."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = OPS_MODULE + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          os.path.join(PKG, "binding", "ops_module.cpp"), "-I", os.path.join(ROOT, "include"),
+          "-isystem", os.path.join(base, "include"),
+          "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-L", os.path.join(base, "lib"), "-L", PKG,
+          "-l:libmoe_layer.so", "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", "-o", tmp])
+    os.replace(tmp, OPS_MODULE)
+    return OPS_MODULE
+
+
 def build_all(verbose=False):
-    return build_layer(verbose), build_synth(), build_synth_host(), build_peaks()
+    return build_layer(verbose), build_synth(), build_synth_host(), build_peaks(), build_ops_module()
 
 
 if __name__ == "__main__":

@@ -173,6 +173,16 @@ def test_strided_codes_and_output(M):
     close(y, want, tol + EPS32 * want.abs())
 
 
+def test_rows_without_tokens():
+    """A permutation of rows that no token backs: rows of zeros, for bf16 tokens and for codes."""
+    w, ws = codes(1, 2, 32, 64).cuda(), scales(2, 2, 32).cuda()
+    off, perm = offsets_of([3, 40]).cuda(), torch.arange(43, dtype=torch.int32, device="cuda")
+    for x, xs in ((torch.empty(0, 64, dtype=BF16, device="cuda"), None),
+                  (torch.empty(0, 64, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda"))):
+        y = ops.grouped_matmul_i8(x, w, ws, off, perm=perm, top_k=2, x_scale=xs)
+        assert y.shape == (43, 32) and (y == 0).all()
+
+
 def test_no_rows_and_refusals():
     w, ws = codes(1, 32, 64).cuda(), scales(2, 32).cuda()
     assert ops.matmul_i8(torch.empty(0, 64, dtype=BF16, device="cuda"), w, ws).shape == (0, 32)
