@@ -57,8 +57,8 @@ typedef struct {
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP32 = 1 } moe_dtype_t;
 
 /* Shapes of the bf16 products: N and K multiples of 8, 8 <= N <= 2^20,
- * 8 <= K <= 16384, ldx and ldy multiples of 8, rows and x_rows < 2^31, and
- * at most 2^22 output tiles of 256 x 256.  Products accumulate in fp32 and
+ * 8 <= K <= 16384, ldx and ldy multiples of 8 and at most 2^20, rows and
+ * x_rows < 2^31, and at most 2^22 output tiles of 256 x 256.  Products accumulate in fp32 and
  * are rounded once to the output's type. */
 
 /* y[p][n] = sum_k x[row(p)][k] w[e][n][k].  x bf16 [x_rows][ldx], w bf16

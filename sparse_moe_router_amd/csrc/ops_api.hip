@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 constexpr int kMaxN = 1 << 20, kMaxK = 16384;
+constexpr int64_t kMaxLd = 1 << 20;  // 256 rows stay within the range of a buffer descriptor
 
 // The matrix-vector kernel takes calls that average at most this many rows an
 // expert, the matrix-matrix kernel the others.
@@ -39,7 +40,7 @@ moe_status_t check_groups(const moe_groups_t* d, int k_unit, int ldx_unit, Check
   if (d->top_k < 1 || d->top_k > kMaxTopK) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (d->ldx < d->K || d->ldy < d->N) return MOE_ERR_INVALID_ARG;
   if (d->ldx % ldx_unit || d->ldy % 8) return MOE_ERR_MISALIGNED;
-  if (d->ldx > ((int64_t)1 << 31) || d->ldy > ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (d->ldx > kMaxLd || d->ldy > kMaxLd) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!d->offsets && d->E != 1) return MOE_ERR_INVALID_ARG;
   if (!aligned(d->offsets, 4) || !aligned(d->perm, 4)) return MOE_ERR_MISALIGNED;
   c->g = Groups{d->rows, d->x_rows, d->ldx, d->ldy, d->E, d->N, d->K, d->top_k, d->offsets, d->perm};

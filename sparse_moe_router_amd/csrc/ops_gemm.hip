@@ -24,12 +24,9 @@
 namespace moe {
 namespace {
 
-constexpr int TB = kOpTile;        // tile edge
-constexpr int SU = TB * 8;         // 16-byte units of one stage (32 KB)
-constexpr int DA = 2, DB = 3;      // stages of the two rings
-
-// where transfers of rows, columns or reduction steps past the end read zeros
-__device__ __align__(16) const uint32_t kZero[4] = {0, 0, 0, 0};
+constexpr int TB = kOpTile;  // tile edge
+constexpr int HU = 1024;     // 16-byte units of a half-tile stage: 128 rows x 128 bytes, or 64 x 256 (16 KB)
+constexpr int GI = 8192;     // rows of x whose indexes the weight gradient holds in LDS at a time
 
 typedef __attribute__((__vector_size__(4 * sizeof(int16_t)))) int16_t i16x4_t;
 
@@ -44,11 +41,34 @@ struct TileArgs {
   int nrow;    // TN: tiles along n
 };
 
-__device__ __forceinline__ void dma(const char* src, u32x4_t* dst) {
+// Transfers go through range-checked buffer descriptors: a lane whose offset
+// lies past the descriptor's range gets zeros in LDS, so rows, columns and
+// steps past an operand's end need no branches, and a transfer needs one
+// register of address (64-bit addresses took twice the issue time beside the
+// other group's MFMAs: a memory part with two transfers 400 cycles).
+typedef __amdgpu_buffer_rsrc_t window_t;
+constexpr uint32_t kOut = 0x80000000u;    // an offset past every range
+constexpr int64_t kRange = 0x7FFFFFFF;    // largest range of a descriptor
+__device__ __forceinline__ window_t window(const char* base, int64_t bytes) {
+  const int n = bytes < 0 ? 0 : bytes > kRange ? (int)kRange : (int)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, n, 0x00020000);
+}
+__device__ __forceinline__ void dma(window_t w, uint32_t off, int step_off, u32x4_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(w, (__attribute__((address_space(3))) void*)dst, 16, (int)off, step_off, 0, 0);
+}
+// by 64-bit addresses, for rows of x that lie more than a descriptor's range apart
+__device__ __align__(16) const uint32_t kZero[4] = {0, 0, 0, 0};
+__device__ __forceinline__ void dma64(const char* src, u32x4_t* dst) {
   __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+// waits until at most N of the wave's transfers are in flight and its LDS reads are done
 template <int N>
 __device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt(N) lgkmcnt(0)
 }
 __device__ __forceinline__ void bar() {
@@ -58,8 +78,8 @@ __device__ __forceinline__ void bar() {
 }
 
 // The row tile and panel of workgroup (xcd, local): group, first row, rows.  A
-// group of c rows has ceil(c / 256) tiles of equal height (a multiple of 32);
-// the units (tile, panel), panels of a tile in a row, are cut into eight equal
+// group of c rows has ceil(c / 256) tiles, all of 256 rows but the last; the
+// units (tile, panel), panels of a tile in a row, are cut into eight equal
 // runs, one for each XCD.  Lane l scans the groups [l * per, (l + 1) * per);
 // every wave does the same scan.
 struct RowTile {
@@ -110,145 +130,208 @@ __device__ __forceinline__ bool find_tile(const Groups& g, int xcd, int64_t loca
       i -= n;
     }
   }
-  const int64_t nt = (c + TB - 1) / TB;
-  const int64_t h = ((c + nt - 1) / nt + 31) / 32 * 32;
-  const int64_t p0 = lo + i * h;
+  const int64_t p0 = lo + i * TB;
   out->e = __builtin_amdgcn_readfirstlane(e);
-  out->p0 = ((int64_t)__builtin_amdgcn_readfirstlane((int)(p0 >> 32)) << 32) |
-            (uint32_t)__builtin_amdgcn_readfirstlane((int)p0);
-  out->rows = __builtin_amdgcn_readfirstlane((int)(c - i * h < h ? c - i * h : h));
+  out->p0 = uniform64(p0);
+  out->rows = __builtin_amdgcn_readfirstlane((int)(c - i * TB < TB ? c - i * TB : TB));
   out->panel = __builtin_amdgcn_readfirstlane((int)(unit - t * npan));
   return true;
 }
 
-// One output tile.  Wave w = 4 rg + cg: columns [64 cg, +64) in two blocks of
-// 32, rows in the 32-row blocks rb = rg, rg + 2, ... below NRB.
-template <OpKind KIND, bool I8, int NRB>
+// LDS of a tile: eight half-tile stages and four half-high ones, distinct
+// arrays so that the compiler can tell a read of one stage from the transfers
+// still in flight into the others.
+struct Lds {
+  u32x4_t* h[8];  // HU units each
+  u32x4_t* q[4];  // HU / 2 units each
+};
+
+// One output tile, eight waves: wm = wave / 4, wn = wave % 4.  The tile's rows
+// come in two halves of 64 RB0 and 64 RB1 rows (RB1 may be 0), its 256 columns
+// in two halves of 128; wave (wm, wn) has rows [32 RB wm, +32 RB) of each row
+// half and 32 columns of each column half: four quadrants.
+//
+// A K-step runs as one cluster per quadrant: a memory part (LDS reads of the
+// quadrant's operands, transfers for a later step) and a multiply part, each
+// closed by a barrier.  The waves wm = 1 run one barrier behind those with
+// wm = 0, the two waves of a SIMD being one of each: while one multiplies the
+// other reads, so the matrix unit, the LDS and the transfers work at the same
+// time without competing for the SIMD's issue.
+//
+// Stages hold whole steps; with both row halves there are two of them (128 KB),
+// with one half three, with a quarter four.  A half-tile is refilled as soon as
+// both groups have read it (the second group reads one barrier later), so
+// every transfer has at least 1.5 steps to land; every wave waits for its own
+// part (a count of the transfers issued after it) at a barrier before the
+// first group reads it.  Transfers are never conditional: those of steps past
+// the end read zeros into a stage nobody reads.
+// G64: gathered rows of x by 64-bit addresses.
+template <OpKind KIND, bool I8, int RB0, int RB1, bool G64>
 __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p0, int rows, int64_t len, int r0t,
-                                             int panel, u32x4_t* const (&ra)[DA], u32x4_t* const (&rb_)[DB]) {
+                                             int panel, const Lds& lds, int32_t* gidx) {
   constexpr bool AT = KIND == OP_TN, BT = KIND != OP_NT;  // operand reduces across its rows
-  constexpr int NRH = (NRB + 1) / 2;
-  constexpr int ES = I8 ? 1 : 2;           // bytes an element
+  constexpr int ES = I8 ? 1 : 2;                          // bytes an element
+  constexpr int ST = RB1 > 0 ? 2 : RB0 == 2 ? 3 : 4;      // stages
+  constexpr int RBM = RB0 > RB1 ? RB0 : RB1;
+  static_assert(!AT || (RB0 == 2 && RB1 == 2), "weight gradients have full tiles");
   typedef typename std::conditional<I8, i32x16_t, f32x16_t>::type acc_t;
   const Groups& g = p.g;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int cg = wave & 3, rg = wave >> 2;
-  const int lr = lane >> 3;
-  const char* zero = (const char*)kZero;
+  const int wn = wave & 3, wm = wave >> 2;
 
-  // output tile: rows of `ncols`-wide out starting at (row base, c0)
+  // ---- LDS of the stages
+  u32x4_t *sa[2][ST], *sb[2][ST];
+#pragma unroll
+  for (int d = 0; d < ST; ++d) {
+    sb[0][d] = lds.h[2 * d];
+    sb[1][d] = lds.h[2 * d + 1];
+    if (ST == 2) {
+      sa[0][d] = lds.h[4 + d];
+      sa[1][d] = lds.h[6 + d];
+    } else if (ST == 3) {
+      // the third in two parts: the 64 rows that the waves with wm = 0 fill and read, and the others'
+      sa[0][d] = d < 2 ? lds.h[6 + d] : (wm ? lds.q[1] : lds.q[0]);
+    } else {
+      sa[0][d] = lds.q[d];
+    }
+  }
+
   const int ncols = KIND == OP_NT ? g.N : g.K;
   const int c0 = panel * TB;
-  // reduction length in elements; steps of 128 bytes (64 rows where it runs across rows)
-  const int64_t red = KIND == OP_NT ? g.K : KIND == OP_NN ? g.N : len;
-  constexpr int BKE = I8 ? 128 : 64;
-  const int nsteps = (int)((red + BKE - 1) / BKE);
+  constexpr int BKE = I8 ? 128 : 64;  // reduction elements of a step
+  // first column of the tile's 32-column block wn of column half j.  Weights read along memory: a
+  // wave's two blocks side by side, so that it writes whole cache lines; across: halves of 128.
+  auto col_of = [&](int j, int blk) { return BT ? 128 * j + 32 * blk : 64 * blk + 32 * j; };
 
-  // ---- transfers.  Along-memory operand: transfer i of the wave fills stage
-  // rows 8 blk .. +8 (blk = wave * n + i), lane -> row lane/8, chunk
-  // position lane%8, source chunk (lane%8) ^ ((row/2) % 8), the swizzle that
-  // spreads 16 consecutive rows' reads over all banks.  Across-rows operand:
-  // transfer i fills stage rows 2 blk, +1 (512 bytes each), lane -> row
-  // lane/32, chunk position lane%32, source chunk pos ^ 4 (row % 4): the four
+  // ---- transfers.  Along-memory operand: a transfer fills 8 stage rows of 128
+  // bytes, lane -> row lane/8, chunk position lane%8, source chunk
+  // (lane%8) ^ ((row/2) % 8): 16 consecutive rows' reads then fall on all
+  // banks.  Across-rows operand: 4 stage rows of 256 bytes, lane -> row
+  // lane/16, position lane%16, source chunk position ^ 4 (row % 4): the four
   // rows a transposing read takes together lie in different 64-byte parts.
-  // A lane's transfers of steps >= lim read zeros.
-  const char* asrc[4];
-  int alim[4];
-  int64_t astep;
-  if (!AT) {
-    astep = 128;
-    const int64_t ld = KIND == OP_NT ? g.ldx : g.ldy;
-#pragma unroll
-    for (int i = 0; i < NRH; ++i) {
-      const int blk = wave * NRH + i, row = blk * 8 + lr;
-      const int q = (lane & 7) ^ ((row >> 1) & 7);
-      int64_t src = -1;
-      if (row < rows) src = KIND == OP_NT ? source_row(g, p0 + row) : p0 + row;
-      const int64_t rest = red - (int64_t)q * (16 / ES);  // elements from this chunk on
-      asrc[i] = p.a + (src < 0 ? 0 : src) * ld * ES + q * 16;
-      alim[i] = src < 0 || rest <= 0 ? 0 : (int)((rest + BKE - 1) / BKE);
+  const int lr = lane >> 3;
+  const bool gather = KIND != OP_NN && g.perm;
+  const int64_t lda = KIND == OP_NT ? g.ldx : g.ldy;
+  int64_t red = KIND == OP_NT ? g.K : KIND == OP_NN ? g.N : len;  // reduction length (TN: of this chunk)
+  int64_t base = p0;                                              // TN: first row of the chunk
+  int nsteps = 0;
+  // window of the first step, and what a step adds to its base (across) or to the offsets (along: 128)
+  const char *abase, *bbase;
+  int64_t abytes, bbytes;
+  const int64_t astep = g.ldy * 128, bstep = (KIND == OP_NN ? (int64_t)g.K : g.ldx) * 128;
+  uint32_t aoff[2][RBM], boff[2][2];  // a lane's offsets in its window
+  bool aend[2][RBM], bend[2][2];      // along: the lane's chunk lies in the last step
+  const char* a64[2][RBM];
+  auto set_sources = [&]() {
+    nsteps = (int)((red + BKE - 1) / BKE);
+    const int last = (int)(red - (int64_t)(nsteps - 1) * BKE);  // elements of the last step
+    if (AT) {
+      abase = p.a + base * g.ldy * 2;
+      abytes = ((red - 1) * g.ldy + g.N) * 2;
+    } else {
+      abase = p.a + (gather ? 0 : p0 * lda * ES);
+      abytes = (((gather ? g.x_rows : rows) - 1) * lda + red) * ES;
     }
-  } else {
-    astep = (int64_t)64 * g.ldy * 2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (wave * 4 + i) * 2 + half;
-      const int col = r0t * TB + (l32 ^ (4 * (row & 3))) * 8;
-      asrc[i] = p.a + ((p0 + row) * g.ldy + col) * 2;
-      alim[i] = col >= g.N || row >= len ? 0 : (int)((len - row + 63) / 64);
+    if (KIND == OP_NT) {
+      bbase = p.b + ((int64_t)e * g.N + c0) * g.K * ES;
+      bbytes = (int64_t)(g.N - c0) * g.K * ES;
+    } else if (KIND == OP_NN) {
+      bbase = p.b + (int64_t)e * g.N * g.K * 2;
+      bbytes = (int64_t)g.N * g.K * 2;
+    } else {
+      bbase = p.b + (gather ? 0 : base * g.ldx * 2);
+      bbytes = (((gather ? g.x_rows : red) - 1) * g.ldx + g.K) * 2;
     }
-  }
-  const char* bsrc[4];
-  int blim[4];
-  int64_t bstep;
-  int bcol = 0;
-  if (!BT) {
-    bstep = 128;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (wave * 4 + i) * 8 + lr;
-      const int q = (lane & 7) ^ ((row >> 1) & 7);
-      const int n = c0 + row;
-      const int64_t rest = red - (int64_t)q * (16 / ES);
-      bsrc[i] = p.b + (((int64_t)e * g.N + (n < g.N ? n : 0)) * g.K) * ES + q * 16;
-      blim[i] = n >= g.N || rest <= 0 ? 0 : (int)((rest + BKE - 1) / BKE);
-    }
-  } else if (KIND == OP_NN) {
-    bstep = (int64_t)64 * g.K * 2;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (wave * 4 + i) * 2 + half;
-      const int col = c0 + (l32 ^ (4 * (row & 3))) * 8;
-      bsrc[i] = p.b + (((int64_t)e * g.N + row) * g.K + col) * 2;
-      blim[i] = col >= g.K || row >= g.N ? 0 : (g.N - row + 63) / 64;
-    }
-  } else {
-    bstep = (int64_t)64 * g.ldx * 2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (wave * 4 + i) * 2 + half;
-      const int col = c0 + (l32 ^ (4 * (row & 3))) * 8;
-      bcol = col;
-      bsrc[i] = p.b + (g.perm ? (int64_t)col * 2 : ((p0 + row) * g.ldx + col) * 2);
-      blim[i] = col >= g.K || row >= len ? 0 : (int)((len - row + 63) / 64);
-    }
-  }
-  (void)bcol;
-  auto load_a = [&](int st, int s) {
-#pragma unroll
-    for (int i = 0; i < (AT ? 4 : NRH); ++i)
-      dma(s < alim[i] ? asrc[i] + s * astep : zero, ra[st] + (wave * (AT ? 4 : NRH) + i) * 64);
-  };
-  // TN with a permutation: the rows of x that the lane's transfers of step s read
-  auto gather = [&](int64_t (&idx)[4], int s) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = (int64_t)s * 64 + (wave * 4 + i) * 2 + half;
-      idx[i] = s < blim[i] ? source_row(g, p0 + r) : -1;
-    }
-  };
-  auto load_b = [&](int st, int s, const int64_t (&idx)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const char* src = zero;
-      if (KIND == OP_TN && g.perm) {
-        if (idx[i] >= 0) src = bsrc[i] + idx[i] * g.ldx * 2;
-      } else if (s < blim[i]) {
-        src = bsrc[i] + s * bstep;
+      for (int i = 0; i < RBM; ++i) {
+        if (i >= (h ? RB1 : RB0)) continue;
+        if (!AT) {
+          const int srow = (wave * (h ? RB1 : RB0) + i) * 8 + lr, row = (h ? 64 * RB0 : 0) + srow;
+          const int q = (lane & 7) ^ ((srow >> 1) & 7);
+          aend[h][i] = q * (16 / ES) < last;
+          if (gather) {
+            const int64_t t = row < rows ? source_row(g, p0 + row) : -1;
+            if (G64)
+              a64[h][i] = t < 0 ? nullptr : p.a + t * lda * ES + q * 16;
+            else
+              aoff[h][i] = t < 0 ? kOut : (uint32_t)(t * lda * ES + q * 16);
+          } else {
+            aoff[h][i] = (uint32_t)(row * lda * ES + q * 16);  // rows past the tile's lie past the range
+          }
+        } else {
+          const int row = (wave * 2 + i) * 4 + (lane >> 4);
+          const int col = r0t * TB + 128 * h + ((lane & 15) ^ (4 * (row & 3))) * 8;
+          aoff[h][i] = col >= g.N ? kOut : (uint32_t)((row * g.ldy + col) * 2);
+        }
       }
-      dma(src, rb_[st] + (wave * 4 + i) * 64);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!BT) {
+          const int srow = (wave * 2 + i) * 8 + lr;
+          const int q = (lane & 7) ^ ((srow >> 1) & 7);
+          bend[j][i] = q * (16 / ES) < last;
+          // rows past N lie past the range
+          boff[j][i] = (uint32_t)((col_of(j, srow >> 5) + (srow & 31)) * g.K * ES + q * 16);
+        } else {
+          const int row = (wave * 2 + i) * 4 + (lane >> 4);
+          const int col = c0 + 128 * j + ((lane & 15) ^ (4 * (row & 3))) * 8;
+          const int64_t ld = KIND == OP_NN ? (int64_t)g.K : gather ? 0 : g.ldx;
+          boff[j][i] = col >= g.K ? kOut : (uint32_t)((row * ld + col) * 2);
+        }
+      }
+  };
+  auto split = [&](int st) { return ST == 3 && st == 2; };  // the stage in two parts
+  auto load_a = [&](int h, int st, int s) {
+    const int sc = s < nsteps ? s : nsteps - 1;
+#pragma unroll
+    for (int i = 0; i < RBM; ++i) {
+      if (i >= (h ? RB1 : RB0)) continue;
+      u32x4_t* dst = sa[h][st] + ((split(st) ? wn : wave) * (h ? RB1 : RB0) + i) * 64;
+      if (AT) {
+        dma(window(abase + s * astep, abytes - s * astep), aoff[h][i], 0, dst);
+      } else if (G64 && gather) {
+        dma64(a64[h][i] && (s < nsteps - 1 || aend[h][i]) ? a64[h][i] + sc * 128 : (const char*)kZero, dst);
+      } else {
+        dma(window(abase, abytes), s >= nsteps - 1 && !aend[h][i] ? kOut : aoff[h][i], sc * 128, dst);
+      }
+    }
+  };
+  auto load_b = [&](int j, int st, int s) {
+    const int sc = s < nsteps ? s : nsteps - 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u32x4_t* dst = sb[j][st] + (wave * 2 + i) * 64;
+      if (!BT) {
+        dma(window(bbase, bbytes), s >= nsteps - 1 && !bend[j][i] ? kOut : boff[j][i], sc * 128, dst);
+      } else if (KIND == OP_TN && gather) {
+        // rows past the end have no index: -1
+        const int32_t t = gidx[sc * 64 + (wave * 2 + i) * 4 + (lane >> 4)];
+        const bool in = t >= 0 && boff[j][i] != kOut;
+        if (G64)
+          dma64(in ? bbase + (int64_t)t * g.ldx * 2 + boff[j][i] : (const char*)kZero, dst);
+        else
+          dma(window(bbase, bbytes), in ? (uint32_t)(t * (int)g.ldx * 2) + boff[j][i] : kOut, 0, dst);
+      } else {
+        dma(window(bbase + s * bstep, bbytes - s * bstep), boff[j][i], 0, dst);
+      }
     }
   };
 
-  acc_t acc[NRH][2];
+  acc_t acc[2][RBM][2];  // [row half][block][column half]
 #pragma unroll
-  for (int j = 0; j < NRH; ++j)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) acc[j][c] = (acc_t){};
+    for (int b = 0; b < RBM; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[h][b][j] = (acc_t){};
 
-  // ---- operand reads: sub-step kk, lane half h take the reduction elements
-  // 32 h + 8 kk .. +8 of a step (int8: 64 h + 16 kk .. +16) on both operands.
+  // ---- operand reads: sub-step kk, lane half take the reduction elements
+  // 32 half + 8 kk .. +8 of a step (int8: 64 half + 16 kk .. +16) on both operands
   auto read_along = [&](const u32x4_t* st, int row32, int kk) -> u32x4_t {
     return st[(row32 + l32) * 8 + ((4 * half + kk) ^ ((l32 >> 1) & 7))];
   };
@@ -257,90 +340,147 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     // two transposing reads of 4 rows each; lane ti of 16 supplies row ti/4, columns 4 (ti%4) .. +4
     const int row = 32 * half + 8 * kk + (ti >> 2);
     const int q = (col32 / 8 + 2 * tsub + ((ti & 3) >> 1)) ^ (4 * (ti >> 2));
-    const char* at = (const char*)(st + row * 32 + q) + 8 * (ti & 1);
-    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)at);
-    const i16x4_t hi =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(at + 4 * 512));
-    u32x4_t r;
-    const uint64_t l64 = __builtin_bit_cast(uint64_t, lo), h64 = __builtin_bit_cast(uint64_t, hi);
-    r[0] = (uint32_t)l64;
-    r[1] = (uint32_t)(l64 >> 32);
-    r[2] = (uint32_t)h64;
-    r[3] = (uint32_t)(h64 >> 32);
-    return r;
+    const char* at = (const char*)(st + row * 16 + q) + 8 * (ti & 1);
+    const uint64_t lo = __builtin_bit_cast(
+        uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)at));
+    const uint64_t hi = __builtin_bit_cast(
+        uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(at + 4 * 256)));
+    return u32x4_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  };
+  u32x4_t af[RBM][4], bf[2][4];
+  auto read_a = [&](int h, int st) {
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int b = 0; b < RBM; ++b) {
+        if (b >= (h ? RB1 : RB0)) continue;
+        const int r = 32 * ((h ? RB1 : RB0) * (split(st) ? 0 : wm) + b);
+        af[b][kk] = AT ? read_across(sa[h][st], r, kk) : read_along(sa[h][st], r, kk);
+      }
+  };
+  auto read_b = [&](int j, int st) {
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+      bf[j][kk] = BT ? read_across(sb[j][st], 32 * wn, kk) : read_along(sb[j][st], 32 * wn, kk);
+  };
+  // the multiply part of a cluster, between its two barriers
+  auto multiply = [&](int h, int j) {
+    bar();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int b = 0; b < RBM; ++b) {
+        if (b >= (h ? RB1 : RB0)) continue;
+        if constexpr (I8)
+          acc[h][b][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, af[b][kk]),
+                                                               __builtin_bit_cast(i32x4_t, bf[j][kk]), acc[h][b][j], 0,
+                                                               0, 0);
+        else
+          acc[h][b][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, af[b][kk]),
+                                                                 __builtin_bit_cast(bf16x8_t, bf[j][kk]), acc[h][b][j],
+                                                                 0, 0, 0);
+      }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    bar();
   };
 
-  if (nsteps > 0) {
-    int64_t idx[2][4];
+  // One pass over the reduction; weight gradients with gathered rows pass in
+  // chunks whose row indexes fit the LDS.
+  for (int64_t done = 0; KIND != OP_TN ? done == 0 : done < len; done += GI) {
     if (KIND == OP_TN && g.perm) {
-      gather(idx[0], 0);
-      gather(idx[1], 1);
+      red = len - done < GI ? len - done : GI;
+      base = p0 + done;
+      // up to a whole number of steps, rows past the end as -1
+      for (int i = tid; i < (red + 63) / 64 * 64; i += 512) gidx[i] = i < red ? (int32_t)source_row(g, base + i) : -1;
+      __syncthreads();
+    } else if (done > 0) {
+      break;
     }
-    load_b(0, 0, idx[0]);
-    load_b(1, 1, idx[1]);
-    load_a(0, 0);
-    if (KIND == OP_TN && g.perm) gather(idx[0], 2);
-    for (int s0 = 0; s0 < nsteps; s0 += DA * DB) {
+    set_sources();
+    if constexpr (RB1 > 0) {
+      load_a(0, 0, 0);
+      load_b(0, 0, 0);
+      load_b(1, 0, 0);
+      load_a(1, 0, 0);
+      load_a(0, 1, 1);
+      load_b(0, 1, 1);
+      load_b(1, 1, 1);
+      wait_vm<6 + RB0 + RB1>();
+      bar();
+      if (wm == 1) bar();
+      for (int s0 = 0; s0 < nsteps; s0 += 2) {
 #pragma unroll
-      for (int u = 0; u < DA * DB; ++u) {
-        const int s = s0 + u;
-        if (s >= nsteps) break;  // uniform
-        // own transfers of step s done (at s = 0 all; else after them only
-        // B step s + 1's four were issued), then everyone's
-        if (s == 0)
-          wait_vm<0>();
-        else
-          wait_vm<4>();
-        bar();
-        if (KIND == OP_TN && g.perm) gather(idx[(u + 1) & 1], s + 3);
-        load_a((u + 1) % DA, s + 1);
-        load_b((u + 2) % DB, s + 2, idx[u & 1]);
-        const u32x4_t* sa = ra[u % DA];
-        const u32x4_t* sb = rb_[u % DB];
+        for (int u = 0; u < 2; ++u) {
+          const int s = s0 + u;
+          if (s >= nsteps) break;  // uniform
+          read_a(0, u);
+          read_b(0, u);
+          __builtin_amdgcn_sched_barrier(0);
+          load_a(1, u ^ 1, s + 1);
+          wait_vm<4 + RB0 + 2 * RB1>();  // second column half of this step
+          multiply(0, 0);
+          read_b(1, u);
+          __builtin_amdgcn_sched_barrier(0);
+          load_a(0, u, s + 2);
+          wait_vm<4 + 2 * RB0 + RB1>();  // second row half of this step
+          multiply(0, 1);
+          read_a(1, u);
+          __builtin_amdgcn_sched_barrier(0);
+          load_b(0, u, s + 2);
+          wait_vm<63>();
+          multiply(1, 0);
+          load_b(1, u, s + 2);
+          wait_vm<6 + RB0 + RB1>();  // first halves of the next step
+          multiply(1, 1);
+        }
+      }
+    } else {
+      constexpr int W = (ST - 1) * (RB0 + 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          u32x4_t af[NRH], bf[2];
+      for (int d = 0; d < ST; ++d) {
+        load_a(0, d, d);
+        load_b(0, d, d);
+        if (d < ST - 1) load_b(1, d, d);
+      }
+      wait_vm<W>();
+      bar();
+      if (wm == 1) bar();
+      for (int s0 = 0; s0 < nsteps; s0 += ST) {
 #pragma unroll
-          for (int j = 0; j < NRH; ++j) {
-            const int rb = 2 * j + rg;
-            if (NRB == 1 && rg == 1) continue;
-            af[j] = AT ? read_across(sa, 32 * rb, kk) : read_along(sa, 32 * rb, kk);
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int cb = 64 * cg + 32 * c;
-            bf[c] = BT ? read_across(sb, cb, kk) : read_along(sb, cb, kk);
-          }
-#pragma unroll
-          for (int j = 0; j < NRH; ++j) {
-            if (NRB == 1 && rg == 1) continue;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if constexpr (I8)
-                acc[j][c] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, af[j]),
-                                                                  __builtin_bit_cast(i32x4_t, bf[c]), acc[j][c], 0, 0, 0);
-              else
-                acc[j][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, af[j]),
-                                                                    __builtin_bit_cast(bf16x8_t, bf[c]), acc[j][c], 0,
-                                                                    0, 0);
-            }
-          }
+        for (int u = 0; u < ST; ++u) {
+          const int s = s0 + u;
+          if (s >= nsteps) break;  // uniform
+          read_a(0, u);
+          read_b(0, u);
+          __builtin_amdgcn_sched_barrier(0);
+          load_b(1, (u + ST - 1) % ST, s + ST - 1);
+          wait_vm<W>();  // second column half of this step
+          multiply(0, 0);
+          read_b(1, u);
+          __builtin_amdgcn_sched_barrier(0);
+          load_a(0, u, s + ST);
+          load_b(0, u, s + ST);
+          wait_vm<W>();  // first halves of the next step
+          multiply(0, 1);
         }
       }
     }
+    if (wm == 0) bar();
+    // transfers of steps past the end have landed and every wave has read its
+    // last operands before the LDS is used again
+    wait_vm<0>();
+    bar();
   }
-  // transfers of steps past the end have landed and every wave has read its
-  // last operands before the rings are used again
-  wait_vm<0>();
-  bar();
 
   // ---- epilogue.  Block layout: lane -> column lane%32, register r -> row
   // 8 (r/4) + 4 (lane/32) + r%4.
   const int nrows = KIND == OP_TN ? (g.N - r0t * TB < TB ? g.N - r0t * TB : TB) : rows;
   const int64_t ldo = KIND == OP_NT ? g.ldy : KIND == OP_NN ? g.ldx : g.K;
   const int64_t row_base = KIND == OP_TN ? (int64_t)e * g.N + (int64_t)r0t * TB : p0;
-  const int wc0 = c0 + 64 * cg;
-  float* s_scale = (float*)ra[1];  // I8: the rows' scales
+  float* s_scale = (float*)lds.h[0];  // I8: the rows' scales
   if (I8) {
     if (tid < rows) {
       const int64_t t = source_row(g, p0 + tid);
@@ -351,93 +491,93 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   float ws[2] = {1.0f, 1.0f}, bi[2] = {0.0f, 0.0f};
   if (I8) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int n = wc0 + 32 * c + l32;
+    for (int j = 0; j < 2; ++j) {
+      const int n = c0 + col_of(j, wn) + l32;
       if (n < ncols) {
-        ws[c] = p.sc.w[(int64_t)e * g.N + n];
-        if (p.sc.bias) bi[c] = p.sc.bias[n];
+        ws[j] = p.sc.w[(int64_t)e * g.N + n];
+        if (p.sc.bias) bi[j] = p.sc.bias[n];
       }
     }
   }
-  if (wc0 >= ncols || (NRB == 1 && rg == 1)) return;
-  uint16_t* stage = (uint16_t*)ra[0] + wave * (32 * 64);  // 4 KB a wave
+  uint16_t* stage = (uint16_t*)(wave < 4 ? lds.h[2] : lds.h[3]) + wn * (32 * 64);  // 4 KB a wave
 #pragma unroll
-  for (int j = 0; j < NRH; ++j) {
-    const int rb = 2 * j + rg;
-    if (32 * rb >= nrows) break;  // uniform
-    float v[2][16];
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int b = 0; b < RBM; ++b) {
+      if (b >= (h ? RB1 : RB0)) continue;
+      const int row0 = (h ? 64 * RB0 : 0) + 32 * ((h ? RB1 : RB0) * wm + b);
+      if (row0 >= nrows) continue;  // uniform
+      float v[2][16];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if constexpr (I8) {
-          const int row = 32 * rb + 8 * (r >> 2) + 4 * half + (r & 3);
-          v[c][r] = (float)acc[j][c][r] * (s_scale[row] * ws[c]) + bi[c];
-        } else {
-          v[c][r] = acc[j][c][r];
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          if constexpr (I8) {
+            const int row = row0 + 8 * (r >> 2) + 4 * half + (r & 3);
+            v[j][r] = (float)acc[h][b][j][r] * (s_scale[row] * ws[j]) + bi[j];
+          } else {
+            v[j][r] = acc[h][b][j][r];
+          }
         }
+      if (p.fp32) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = row0 + 8 * (r >> 2) + 4 * half + (r & 3);
+          float* orow = (float*)p.out + (row_base + row) * ldo + c0 + l32;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (row < nrows && c0 + col_of(j, wn) + l32 < ncols) orow[col_of(j, wn)] = v[j][r];
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = 8 * (r >> 2) + 4 * half + (r & 3);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) stage[row * 64 + 32 * j + l32] = (uint16_t)f32_to_bf16(v[j][r]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int c = lane; c < 32 * 8; c += 64) {
+          const int row = c >> 3, q = c & 7;
+          const int grow = row0 + row, col = c0 + col_of(q >> 2, wn) + 8 * (q & 3);
+          if (grow < nrows && col < ncols)
+            *(u32x4_t*)((uint16_t*)p.out + (row_base + grow) * ldo + col) =
+                *(const u32x4_t*)(stage + row * 64 + 8 * q);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
       }
-    if (p.fp32) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = 32 * rb + 8 * (r >> 2) + 4 * half + (r & 3);
-        float* orow = (float*)p.out + (row_base + row) * ldo + wc0 + l32;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (row < nrows && wc0 + 32 * c + l32 < ncols) orow[32 * c] = v[c][r];
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = 8 * (r >> 2) + 4 * half + (r & 3);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) stage[row * 64 + 32 * c + l32] = (uint16_t)f32_to_bf16(v[c][r]);
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-      for (int c = lane; c < 32 * 8; c += 64) {
-        const int row = c >> 3, q = c & 7;
-        const int grow = 32 * rb + row, col = wc0 + 8 * q;
-        if (grow < nrows && col < ncols)
-          *(u32x4_t*)((uint16_t*)p.out + (row_base + grow) * ldo + col) = *(const u32x4_t*)(stage + row * 64 + 8 * q);
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
-  }
 }
 
 // Row-tiled products (NT, NN).  Workgroup b runs on XCD b % 8; a row tile's
 // panels stay on one XCD, whose L2 then serves the tile's rows again.
-template <OpKind KIND, bool I8>
+template <OpKind KIND, bool I8, bool G64>
 __global__ __launch_bounds__(512, 1) void k_op_rows(TileArgs p) {
-  __shared__ u32x4_t sA0[SU], sA1[SU], sB0[SU], sB1[SU], sB2[SU];  // 160 KB
-  u32x4_t* const ra[DA] = {sA0, sA1};
-  u32x4_t* const rb[DB] = {sB0, sB1, sB2};
+  __shared__ u32x4_t h0[HU], h1[HU], h2[HU], h3[HU], h4[HU], h5[HU], h6[HU], h7[HU];  // 128 KB
+  __shared__ u32x4_t q0[HU / 2], q1[HU / 2], q2[HU / 2], q3[HU / 2];                   // 32 KB
+  const Lds lds{{h0, h1, h2, h3, h4, h5, h6, h7}, {q0, q1, q2, q3}};
   RowTile tl;
   if (!find_tile(p.g, blockIdx.x & 7, blockIdx.x >> 3, p.npan, &tl)) return;
-  const int panel = tl.panel;
-  const int nb = (tl.rows + 31) >> 5;
-  if (nb <= 1)
-    tile_product<KIND, I8, 1>(p, tl.e, tl.p0, tl.rows, 0, 0, panel, ra, rb);
-  else if (nb <= 2)
-    tile_product<KIND, I8, 2>(p, tl.e, tl.p0, tl.rows, 0, 0, panel, ra, rb);
-  else if (nb <= 4)
-    tile_product<KIND, I8, 4>(p, tl.e, tl.p0, tl.rows, 0, 0, panel, ra, rb);
-  else if (nb <= 6)
-    tile_product<KIND, I8, 6>(p, tl.e, tl.p0, tl.rows, 0, 0, panel, ra, rb);
+  if (tl.rows > 192)
+    tile_product<KIND, I8, 2, 2, G64>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+  else if (tl.rows > 128)
+    tile_product<KIND, I8, 2, 1, G64>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+  else if (tl.rows > 64)
+    tile_product<KIND, I8, 2, 0, G64>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
   else
-    tile_product<KIND, I8, 8>(p, tl.e, tl.p0, tl.rows, 0, 0, panel, ra, rb);
+    tile_product<KIND, I8, 1, 0, G64>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
 }
 
 // Weight gradients (TN): a workgroup per expert and 256 x 256 tile of dw.
+template <bool G64>
 __global__ __launch_bounds__(512, 1) void k_op_wgrad(TileArgs p) {
-  __shared__ u32x4_t sA0[SU], sA1[SU], sB0[SU], sB1[SU], sB2[SU];
-  u32x4_t* const ra[DA] = {sA0, sA1};
-  u32x4_t* const rb[DB] = {sB0, sB1, sB2};
+  __shared__ u32x4_t h0[HU], h1[HU], h2[HU], h3[HU], h4[HU], h5[HU], h6[HU], h7[HU];
+  __shared__ int32_t gidx[GI];  // 32 KB
+  const Lds lds{{h0, h1, h2, h3, h4, h5, h6, h7}, {nullptr, nullptr, nullptr, nullptr}};
   // an expert's tiles follow one another on one XCD: they share dy and x
   const int per = p.nrow * p.npan;
   const int run = (p.g.E * per + 7) / 8, unit = (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3);
@@ -445,7 +585,9 @@ __global__ __launch_bounds__(512, 1) void k_op_wgrad(TileArgs p) {
   const int e = unit / per, tile = unit % per;
   int64_t lo, hi;
   group_range(p.g, e, &lo, &hi);
-  tile_product<OP_TN, false, 8>(p, e, lo, 0, hi - lo, tile / p.npan, tile % p.npan, ra, rb);
+  lo = uniform64(lo);
+  hi = uniform64(hi);
+  tile_product<OP_TN, false, 2, 2, G64>(p, e, lo, 0, hi - lo, tile / p.npan, tile % p.npan, lds, gidx);
 }
 
 }  // namespace
@@ -469,10 +611,13 @@ hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, 
   t.npan = ((kind == OP_NT ? g.N : g.K) + TB - 1) / TB;
   const unsigned grid = (unsigned)op_tile_units(kind, g);
   const Launch lc{s, nullptr, nullptr};
-  if (kind == OP_TN) return launch(lc, k_op_wgrad, dim3(grid), dim3(512), t);
-  if (kind == OP_NN) return launch(lc, k_op_rows<OP_NN, false>, dim3(grid), dim3(512), t);
-  if (i8) return launch(lc, k_op_rows<OP_NT, true>, dim3(grid), dim3(512), t);
-  return launch(lc, k_op_rows<OP_NT, false>, dim3(grid), dim3(512), t);
+  // gathered rows past the range of a buffer descriptor are fetched by 64-bit addresses
+  const bool far = g.perm && ((g.x_rows - 1) * g.ldx + g.K) * (i8 ? 1 : 2) > kRange;
+  const dim3 gr(grid), bl(512);
+  if (kind == OP_TN) return far ? launch(lc, k_op_wgrad<true>, gr, bl, t) : launch(lc, k_op_wgrad<false>, gr, bl, t);
+  if (kind == OP_NN) return launch(lc, k_op_rows<OP_NN, false, false>, gr, bl, t);
+  if (i8) return far ? launch(lc, k_op_rows<OP_NT, true, true>, gr, bl, t) : launch(lc, k_op_rows<OP_NT, true, false>, gr, bl, t);
+  return far ? launch(lc, k_op_rows<OP_NT, false, true>, gr, bl, t) : launch(lc, k_op_rows<OP_NT, false, false>, gr, bl, t);
 }
 
 }  // namespace moe
