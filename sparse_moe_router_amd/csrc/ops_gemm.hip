@@ -26,6 +26,7 @@ namespace {
 
 constexpr int TB = kOpTile;  // tile edge
 constexpr int HU = 1024;     // 16-byte units of a half-tile stage: 128 rows x 128 bytes, or 64 x 256 (16 KB)
+constexpr int SG = 4;        // row tiles of a block of units
 constexpr int GI = 8192;     // rows of x whose indexes the weight gradient holds in LDS at a time
 
 typedef __attribute__((__vector_size__(4 * sizeof(int16_t)))) int16_t i16x4_t;
@@ -46,20 +47,35 @@ struct TileArgs {
 // steps past an operand's end need no branches, and a transfer needs one
 // register of address (64-bit addresses took twice the issue time beside the
 // other group's MFMAs: a memory part with two transfers 400 cycles).
-typedef __amdgpu_buffer_rsrc_t window_t;
-constexpr uint32_t kOut = 0x80000000u;    // an offset past every range
-constexpr int64_t kRange = 0x7FFFFFFF;    // largest range of a descriptor
+// The transfers are issued by asm statements without outputs: the loop below
+// counts them itself, and the compiler, which tells apart at most eight
+// destinations of transfers in flight, would wait for all of them at every LDS
+// read of a ninth.  A wait of the compiler's own for another load counts later
+// transfers as if they were not there and so only waits longer.  m0, the LDS
+// address of a transfer, is otherwise unused on this architecture but for
+// register indexing, which these kernels have none of; the wait states cover a
+// scalar operand that a vector instruction has just written.
+struct window_t {
+  u32x4_t d;  // buffer descriptor: base, stride 0, range in bytes, raw format
+};
+constexpr uint32_t kOut = 0x80000000u;  // an offset past every range
+constexpr int64_t kRange = 0x7FFFFFFF;  // largest range of a descriptor
 __device__ __forceinline__ window_t window(const char* base, int64_t bytes) {
-  const int n = bytes < 0 ? 0 : bytes > kRange ? (int)kRange : (int)bytes;
-  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, n, 0x00020000);
+  const uint32_t n = bytes < 0 ? 0u : bytes > kRange ? (uint32_t)kRange : (uint32_t)bytes;
+  const uint64_t b = (uint64_t)base;
+  return window_t{u32x4_t{(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, n, 0x00020000u}};
 }
-__device__ __forceinline__ void dma(window_t w, uint32_t off, int step_off, u32x4_t* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(w, (__attribute__((address_space(3))) void*)dst, 16, (int)off, step_off, 0, 0);
+// lane i of the wave writes the 16 bytes at offset off + step_off of the window to LDS address dst + 16 i
+__device__ __forceinline__ void dma(window_t w, uint32_t off, int step_off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst), "v"(off),
+               "s"(w.d), "s"(step_off)
+               : "memory");
 }
 // by 64-bit addresses, for rows of x that lie more than a descriptor's range apart
 __device__ __align__(16) const uint32_t kZero[4] = {0, 0, 0, 0};
-__device__ __forceinline__ void dma64(const char* src, u32x4_t* dst) {
-  __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+__device__ __forceinline__ void dma64(const char* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src)
+               : "memory");
 }
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
@@ -83,12 +99,12 @@ __device__ __forceinline__ void bar() {
 // runs, one for each XCD.  Lane l scans the groups [l * per, (l + 1) * per);
 // every wave does the same scan.
 struct RowTile {
-  int e;
+  int e;  // -1: none
   int64_t p0;
   int rows;
   int panel;
 };
-__device__ __forceinline__ bool find_tile(const Groups& g, int xcd, int64_t local, int npan, RowTile* out) {
+__device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan) {
   const int lane = threadIdx.x & 63;
   int e = 0;
   int64_t lo = 0, c = g.rows, i;
@@ -99,11 +115,7 @@ __device__ __forceinline__ bool find_tile(const Groups& g, int xcd, int64_t loca
   } else {
     for (int j = 0; j < per; ++j) {
       const int ge = lane * per + j;
-      if (ge < g.E) {
-        int64_t a, b;
-        group_range(g, ge, &a, &b);
-        mine += (b - a + TB - 1) / TB;
-      }
+      if (ge < g.E) mine += (group_range(g, ge).size() + TB - 1) / TB;
     }
     incl = mine;
 #pragma unroll
@@ -114,37 +126,29 @@ __device__ __forceinline__ bool find_tile(const Groups& g, int xcd, int64_t loca
     total = __shfl(incl, 63, 64);
   }
   const int64_t run = (total * npan + 7) / 8, unit = xcd * run + local;
-  if (local >= run || unit >= total * npan) return false;
-  const int64_t t = unit / npan;
+  if (local >= run || unit >= total * npan) return RowTile{-1, 0, 0, 0};
+  // within the run, blocks of SG tiles, panel by panel: the 32 workgroups that an XCD runs at a time
+  // then read about as many tiles' rows as panels' weights
+  const int64_t sg = unit / (SG * npan), sr = unit - sg * SG * npan;
+  const int64_t height = total - sg * SG < SG ? total - sg * SG : SG;
+  const int64_t t = sg * SG + sr % height;
   i = t;
   if (g.offsets) {
     const int src = __builtin_ctzll(__ballot(incl > t));
     i -= __shfl(incl - mine, src, 64);
     for (int j = 0; j < per; ++j) {
-      int64_t b;
       e = src * per + j;
-      group_range(g, e, &lo, &b);  // the unit exists, so a group below E holds it
-      c = b - lo;
+      const Range r = group_range(g, e);  // the unit exists, so a group below E holds it
+      lo = r.lo;
+      c = r.size();
       const int64_t n = (c + TB - 1) / TB;
       if (i < n) break;
       i -= n;
     }
   }
   const int64_t p0 = lo + i * TB;
-  out->e = __builtin_amdgcn_readfirstlane(e);
-  out->p0 = uniform64(p0);
-  out->rows = __builtin_amdgcn_readfirstlane((int)(c - i * TB < TB ? c - i * TB : TB));
-  out->panel = __builtin_amdgcn_readfirstlane((int)(unit - t * npan));
-  return true;
+  return RowTile{e, p0, (int)(c - i * TB < TB ? c - i * TB : TB), (int)(sr / height)};
 }
-
-// LDS of a tile: eight half-tile stages and four half-high ones, distinct
-// arrays so that the compiler can tell a read of one stage from the transfers
-// still in flight into the others.
-struct Lds {
-  u32x4_t* h[8];  // HU units each
-  u32x4_t* q[4];  // HU / 2 units each
-};
 
 // One output tile, eight waves: wm = wave / 4, wn = wave % 4.  The tile's rows
 // come in two halves of 64 RB0 and 64 RB1 rows (RB1 may be 0), its 256 columns
@@ -159,16 +163,20 @@ struct Lds {
 // time without competing for the SIMD's issue.
 //
 // Stages hold whole steps; with both row halves there are two of them (128 KB),
-// with one half three, with a quarter four.  A half-tile is refilled as soon as
-// both groups have read it (the second group reads one barrier later), so
-// every transfer has at least 1.5 steps to land; every wave waits for its own
-// part (a count of the transfers issued after it) at a barrier before the
-// first group reads it.  Transfers are never conditional: those of steps past
-// the end read zeros into a stage nobody reads.
-// G64: gathered rows of x by 64-bit addresses.
-template <OpKind KIND, bool I8, int RB0, int RB1, bool G64>
+// with one half three (144 KB), with a quarter four (160 KB).  A half-tile is
+// refilled as soon as both groups have read it (the second group reads one
+// barrier later), so every transfer has more than a step's time to land; every
+// wave waits for its own part (a count of the transfers issued after it) at a
+// barrier before the first group reads it.  Transfers are never conditional:
+// those of steps past the end fetch zeros, or the last step again, into a
+// stage nobody reads.
+//
+// GX: how rows of x are found: GX_ROWS in order (NT: or gathered), GX_INDEX
+// gathered (TN), GX_FAR gathered, by 64-bit addresses.
+enum { GX_ROWS = 0, GX_INDEX = 1, GX_FAR = 2 };
+template <OpKind KIND, bool I8, int RB0, int RB1, int GX>
 __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p0, int rows, int64_t len, int r0t,
-                                             int panel, const Lds& lds, int32_t* gidx) {
+                                             int panel, u32x4_t* lds, int32_t* gidx) {
   constexpr bool AT = KIND == OP_TN, BT = KIND != OP_NT;  // operand reduces across its rows
   constexpr int ES = I8 ? 1 : 2;                          // bytes an element
   constexpr int ST = RB1 > 0 ? 2 : RB0 == 2 ? 3 : 4;      // stages
@@ -180,22 +188,13 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave & 3, wm = wave >> 2;
 
-  // ---- LDS of the stages
-  u32x4_t *sa[2][ST], *sb[2][ST];
-#pragma unroll
-  for (int d = 0; d < ST; ++d) {
-    sb[0][d] = lds.h[2 * d];
-    sb[1][d] = lds.h[2 * d + 1];
-    if (ST == 2) {
-      sa[0][d] = lds.h[4 + d];
-      sa[1][d] = lds.h[6 + d];
-    } else if (ST == 3) {
-      // the third in two parts: the 64 rows that the waves with wm = 0 fill and read, and the others'
-      sa[0][d] = d < 2 ? lds.h[6 + d] : (wm ? lds.q[1] : lds.q[0]);
-    } else {
-      sa[0][d] = lds.q[d];
-    }
-  }
+  // ---- LDS of a stage: the two column halves, then the row halves
+  constexpr int STAGE = 2 * HU + (RB0 + RB1) * HU / 2;
+  static_assert(ST * STAGE <= 10 * HU, "160 KB");
+  // its LDS address, 0 where the array is the kernel's first
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) u32x4_t*)lds;
+  auto sb = [&](int j, int st) { return lds + st * STAGE + j * HU; };
+  auto sa = [&](int h, int st) { return lds + st * STAGE + 2 * HU + (h ? RB0 * HU / 2 : 0); };
 
   const int ncols = KIND == OP_NT ? g.N : g.K;
   const int c0 = panel * TB;
@@ -211,24 +210,31 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   // lane/16, position lane%16, source chunk position ^ 4 (row % 4): the four
   // rows a transposing read takes together lie in different 64-byte parts.
   const int lr = lane >> 3;
-  const bool gather = KIND != OP_NN && g.perm;
+  constexpr bool G64 = GX == GX_FAR;
+  const bool gather = KIND == OP_TN ? GX != GX_ROWS : KIND == OP_NT && g.perm;
   const int64_t lda = KIND == OP_NT ? g.ldx : g.ldy;
   int64_t red = KIND == OP_NT ? g.K : KIND == OP_NN ? g.N : len;  // reduction length (TN: of this chunk)
   int64_t base = p0;                                              // TN: first row of the chunk
-  int nsteps = 0;
+  int nsteps = 0, last = 0;  // steps; reduction elements of the last one
   // window of the first step, and what a step adds to its base (across) or to the offsets (along: 128)
   const char *abase, *bbase;
-  int64_t abytes, bbytes;
+  int64_t abytes = 0, bbytes = 0;
   const int64_t astep = g.ldy * 128, bstep = (KIND == OP_NN ? (int64_t)g.K : g.ldx) * 128;
+  // window of step s of an operand that reduces across its rows: the step's rows that exist
+  auto step_window = [&](const char* at, int64_t step, int s, int width) {
+    const int n = s < nsteps - 1 ? 64 : s == nsteps - 1 ? last : 0;
+    window_t w = window(at + s * step, 0);
+    w.d[2] = n > 0 ? (uint32_t)((n - 1) * (int)(step >> 6) + width) : 0u;
+    return w;
+  };
   uint32_t aoff[2][RBM], boff[2][2];  // a lane's offsets in its window
   bool aend[2][RBM], bend[2][2];      // along: the lane's chunk lies in the last step
   const char* a64[2][RBM];
   auto set_sources = [&]() {
     nsteps = (int)((red + BKE - 1) / BKE);
-    const int last = (int)(red - (int64_t)(nsteps - 1) * BKE);  // elements of the last step
+    last = (int)(red - (int64_t)(nsteps - 1) * BKE);
     if (AT) {
       abase = p.a + base * g.ldy * 2;
-      abytes = ((red - 1) * g.ldy + g.N) * 2;
     } else {
       abase = p.a + (gather ? 0 : p0 * lda * ES);
       abytes = (((gather ? g.x_rows : rows) - 1) * lda + red) * ES;
@@ -238,10 +244,9 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       bbytes = (int64_t)(g.N - c0) * g.K * ES;
     } else if (KIND == OP_NN) {
       bbase = p.b + (int64_t)e * g.N * g.K * 2;
-      bbytes = (int64_t)g.N * g.K * 2;
     } else {
       bbase = p.b + (gather ? 0 : base * g.ldx * 2);
-      bbytes = (((gather ? g.x_rows : red) - 1) * g.ldx + g.K) * 2;
+      bbytes = ((g.x_rows - 1) * g.ldx + g.K) * 2;  // gathered
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -285,15 +290,14 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
         }
       }
   };
-  auto split = [&](int st) { return ST == 3 && st == 2; };  // the stage in two parts
   auto load_a = [&](int h, int st, int s) {
     const int sc = s < nsteps ? s : nsteps - 1;
 #pragma unroll
     for (int i = 0; i < RBM; ++i) {
       if (i >= (h ? RB1 : RB0)) continue;
-      u32x4_t* dst = sa[h][st] + ((split(st) ? wn : wave) * (h ? RB1 : RB0) + i) * 64;
+      const uint32_t dst = lds0 + (sa(h, st) - lds + (wave * (h ? RB1 : RB0) + i) * 64) * 16;
       if (AT) {
-        dma(window(abase + s * astep, abytes - s * astep), aoff[h][i], 0, dst);
+        dma(step_window(abase, astep, s, 2 * g.N), aoff[h][i], 0, dst);
       } else if (G64 && gather) {
         dma64(a64[h][i] && (s < nsteps - 1 || aend[h][i]) ? a64[h][i] + sc * 128 : (const char*)kZero, dst);
       } else {
@@ -305,7 +309,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     const int sc = s < nsteps ? s : nsteps - 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      u32x4_t* dst = sb[j][st] + (wave * 2 + i) * 64;
+      const uint32_t dst = lds0 + (sb(j, st) - lds + (wave * 2 + i) * 64) * 16;
       if (!BT) {
         dma(window(bbase, bbytes), s >= nsteps - 1 && !bend[j][i] ? kOut : boff[j][i], sc * 128, dst);
       } else if (KIND == OP_TN && gather) {
@@ -317,7 +321,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
         else
           dma(window(bbase, bbytes), in ? (uint32_t)(t * (int)g.ldx * 2) + boff[j][i] : kOut, 0, dst);
       } else {
-        dma(window(bbase + s * bstep, bbytes - s * bstep), boff[j][i], 0, dst);
+        dma(step_window(bbase, bstep, s, 2 * g.K), boff[j][i], 0, dst);
       }
     }
   };
@@ -354,14 +358,14 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
 #pragma unroll
       for (int b = 0; b < RBM; ++b) {
         if (b >= (h ? RB1 : RB0)) continue;
-        const int r = 32 * ((h ? RB1 : RB0) * (split(st) ? 0 : wm) + b);
-        af[b][kk] = AT ? read_across(sa[h][st], r, kk) : read_along(sa[h][st], r, kk);
+        const int r = 32 * ((h ? RB1 : RB0) * wm + b);
+        af[b][kk] = AT ? read_across(sa(h, st), r, kk) : read_along(sa(h, st), r, kk);
       }
   };
   auto read_b = [&](int j, int st) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
-      bf[j][kk] = BT ? read_across(sb[j][st], 32 * wn, kk) : read_along(sb[j][st], 32 * wn, kk);
+      bf[j][kk] = BT ? read_across(sb(j, st), 32 * wn, kk) : read_along(sb(j, st), 32 * wn, kk);
   };
   // the multiply part of a cluster, between its two barriers
   auto multiply = [&](int h, int j) {
@@ -390,7 +394,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   // One pass over the reduction; weight gradients with gathered rows pass in
   // chunks whose row indexes fit the LDS.
   for (int64_t done = 0; KIND != OP_TN ? done == 0 : done < len; done += GI) {
-    if (KIND == OP_TN && g.perm) {
+    if (KIND == OP_TN && gather) {
       red = len - done < GI ? len - done : GI;
       base = p0 + done;
       // up to a whole number of steps, rows past the end as -1
@@ -401,15 +405,19 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     }
     set_sources();
     if constexpr (RB1 > 0) {
-      load_a(0, 0, 0);
-      load_b(0, 0, 0);
-      load_b(1, 0, 0);
-      load_a(1, 0, 0);
-      load_a(0, 1, 1);
-      load_b(0, 1, 1);
-      load_b(1, 1, 1);
-      wait_vm<6 + RB0 + RB1>();
+      // memory parts: 8, 4, 8 and 4 reads of a block, two transfers a wave in each.  The first column
+      // half of a step is read in the last part of the step before.
+      constexpr int WB = 6 + RB0 + 2 * RB1, WA = 6 + 2 * RB0 + RB1;
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        load_b(0, d, d);
+        load_a(0, d, d);
+        load_b(1, d, d);
+        load_a(1, d, d);
+      }
+      wait_vm<WB>();  // first halves of step 0
       bar();
+      read_b(0, 0);
       if (wm == 1) bar();
       for (int s0 = 0; s0 < nsteps; s0 += 2) {
 #pragma unroll
@@ -417,36 +425,34 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           const int s = s0 + u;
           if (s >= nsteps) break;  // uniform
           read_a(0, u);
-          read_b(0, u);
-          __builtin_amdgcn_sched_barrier(0);
-          load_a(1, u ^ 1, s + 1);
-          wait_vm<4 + RB0 + 2 * RB1>();  // second column half of this step
+          load_b(0, u, s + 2);
+          wait_vm<WB>();  // second column half of this step
           multiply(0, 0);
           read_b(1, u);
-          __builtin_amdgcn_sched_barrier(0);
           load_a(0, u, s + 2);
-          wait_vm<4 + 2 * RB0 + RB1>();  // second row half of this step
+          wait_vm<WA>();  // second row half of this step
           multiply(0, 1);
           read_a(1, u);
-          __builtin_amdgcn_sched_barrier(0);
-          load_b(0, u, s + 2);
-          wait_vm<63>();
-          multiply(1, 0);
           load_b(1, u, s + 2);
-          wait_vm<6 + RB0 + RB1>();  // first halves of the next step
+          wait_vm<WA>();  // first column half of the next step
+          multiply(1, 0);
+          read_b(0, u ^ 1);
+          load_a(1, u, s + 2);
+          wait_vm<WB>();  // first row half of the next step
           multiply(1, 1);
         }
       }
     } else {
-      constexpr int W = (ST - 1) * (RB0 + 4);
+      constexpr int W = 2 * (ST - 1) + (ST - 2) * (RB0 + 2);
 #pragma unroll
       for (int d = 0; d < ST; ++d) {
         load_a(0, d, d);
         load_b(0, d, d);
         if (d < ST - 1) load_b(1, d, d);
       }
-      wait_vm<W>();
+      wait_vm<W + RB0 + 2>();  // first halves of step 0
       bar();
+      read_b(0, 0);
       if (wm == 1) bar();
       for (int s0 = 0; s0 < nsteps; s0 += ST) {
 #pragma unroll
@@ -454,16 +460,14 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           const int s = s0 + u;
           if (s >= nsteps) break;  // uniform
           read_a(0, u);
-          read_b(0, u);
-          __builtin_amdgcn_sched_barrier(0);
           load_b(1, (u + ST - 1) % ST, s + ST - 1);
-          wait_vm<W>();  // second column half of this step
+          wait_vm<W>();  // second column half of this step, first halves of the next
           multiply(0, 0);
           read_b(1, u);
-          __builtin_amdgcn_sched_barrier(0);
+          read_b(0, (u + 1) % ST);
           load_a(0, u, s + ST);
           load_b(0, u, s + ST);
-          wait_vm<W>();  // first halves of the next step
+          wait_vm<63>();
           multiply(0, 1);
         }
       }
@@ -480,7 +484,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   const int nrows = KIND == OP_TN ? (g.N - r0t * TB < TB ? g.N - r0t * TB : TB) : rows;
   const int64_t ldo = KIND == OP_NT ? g.ldy : KIND == OP_NN ? g.ldx : g.K;
   const int64_t row_base = KIND == OP_TN ? (int64_t)e * g.N + (int64_t)r0t * TB : p0;
-  float* s_scale = (float*)lds.h[0];  // I8: the rows' scales
+  float* s_scale = (float*)lds;  // I8: the rows' scales
   if (I8) {
     if (tid < rows) {
       const int64_t t = source_row(g, p0 + tid);
@@ -499,7 +503,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       }
     }
   }
-  uint16_t* stage = (uint16_t*)(wave < 4 ? lds.h[2] : lds.h[3]) + wn * (32 * 64);  // 4 KB a wave
+  uint16_t* stage = (uint16_t*)(lds + HU) + wave * (32 * 64);  // 4 KB a wave
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -555,39 +559,36 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
 
 // Row-tiled products (NT, NN).  Workgroup b runs on XCD b % 8; a row tile's
 // panels stay on one XCD, whose L2 then serves the tile's rows again.
-template <OpKind KIND, bool I8, bool G64>
+template <OpKind KIND, bool I8, int GX>
 __global__ __launch_bounds__(512, 1) void k_op_rows(TileArgs p) {
-  __shared__ u32x4_t h0[HU], h1[HU], h2[HU], h3[HU], h4[HU], h5[HU], h6[HU], h7[HU];  // 128 KB
-  __shared__ u32x4_t q0[HU / 2], q1[HU / 2], q2[HU / 2], q3[HU / 2];                   // 32 KB
-  const Lds lds{{h0, h1, h2, h3, h4, h5, h6, h7}, {q0, q1, q2, q3}};
-  RowTile tl;
-  if (!find_tile(p.g, blockIdx.x & 7, blockIdx.x >> 3, p.npan, &tl)) return;
+  __shared__ u32x4_t lds[10 * HU];  // 160 KB
+  RowTile tl = find_tile(p.g, blockIdx.x & 7, blockIdx.x >> 3, p.npan);
+  // the same in every lane, which the compiler cannot see behind the scan
+  tl = RowTile{__builtin_amdgcn_readfirstlane(tl.e), uniform64(tl.p0), __builtin_amdgcn_readfirstlane(tl.rows),
+               __builtin_amdgcn_readfirstlane(tl.panel)};
+  if (tl.e < 0) return;
   if (tl.rows > 192)
-    tile_product<KIND, I8, 2, 2, G64>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+    tile_product<KIND, I8, 2, 2, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
   else if (tl.rows > 128)
-    tile_product<KIND, I8, 2, 1, G64>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+    tile_product<KIND, I8, 2, 1, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
   else if (tl.rows > 64)
-    tile_product<KIND, I8, 2, 0, G64>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+    tile_product<KIND, I8, 2, 0, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
   else
-    tile_product<KIND, I8, 1, 0, G64>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+    tile_product<KIND, I8, 1, 0, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
 }
 
 // Weight gradients (TN): a workgroup per expert and 256 x 256 tile of dw.
-template <bool G64>
+template <int GX>
 __global__ __launch_bounds__(512, 1) void k_op_wgrad(TileArgs p) {
-  __shared__ u32x4_t h0[HU], h1[HU], h2[HU], h3[HU], h4[HU], h5[HU], h6[HU], h7[HU];
-  __shared__ int32_t gidx[GI];  // 32 KB
-  const Lds lds{{h0, h1, h2, h3, h4, h5, h6, h7}, {nullptr, nullptr, nullptr, nullptr}};
+  __shared__ u32x4_t lds[8 * HU];
+  __shared__ int32_t gidx[GX == GX_ROWS ? 1 : GI];  // 32 KB
   // an expert's tiles follow one another on one XCD: they share dy and x
   const int per = p.nrow * p.npan;
   const int run = (p.g.E * per + 7) / 8, unit = (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3);
   if (unit >= p.g.E * per) return;
   const int e = unit / per, tile = unit % per;
-  int64_t lo, hi;
-  group_range(p.g, e, &lo, &hi);
-  lo = uniform64(lo);
-  hi = uniform64(hi);
-  tile_product<OP_TN, false, 2, 2, G64>(p, e, lo, 0, hi - lo, tile / p.npan, tile % p.npan, lds, gidx);
+  const Range r = group_range(p.g, e);
+  tile_product<OP_TN, false, 2, 2, GX>(p, e, uniform64(r.lo), 0, uniform64(r.size()), tile / p.npan, tile % p.npan, lds, gidx);
 }
 
 }  // namespace
@@ -614,10 +615,16 @@ hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, 
   // gathered rows past the range of a buffer descriptor are fetched by 64-bit addresses
   const bool far = g.perm && ((g.x_rows - 1) * g.ldx + g.K) * (i8 ? 1 : 2) > kRange;
   const dim3 gr(grid), bl(512);
-  if (kind == OP_TN) return far ? launch(lc, k_op_wgrad<true>, gr, bl, t) : launch(lc, k_op_wgrad<false>, gr, bl, t);
-  if (kind == OP_NN) return launch(lc, k_op_rows<OP_NN, false, false>, gr, bl, t);
-  if (i8) return far ? launch(lc, k_op_rows<OP_NT, true, true>, gr, bl, t) : launch(lc, k_op_rows<OP_NT, true, false>, gr, bl, t);
-  return far ? launch(lc, k_op_rows<OP_NT, false, true>, gr, bl, t) : launch(lc, k_op_rows<OP_NT, false, false>, gr, bl, t);
+  if (kind == OP_TN) {
+    if (!g.perm) return launch(lc, k_op_wgrad<GX_ROWS>, gr, bl, t);
+    return far ? launch(lc, k_op_wgrad<GX_FAR>, gr, bl, t) : launch(lc, k_op_wgrad<GX_INDEX>, gr, bl, t);
+  }
+  if (kind == OP_NN) return launch(lc, k_op_rows<OP_NN, false, GX_ROWS>, gr, bl, t);
+  if (i8)
+    return far ? launch(lc, k_op_rows<OP_NT, true, GX_FAR>, gr, bl, t)
+               : launch(lc, k_op_rows<OP_NT, true, GX_ROWS>, gr, bl, t);
+  return far ? launch(lc, k_op_rows<OP_NT, false, GX_FAR>, gr, bl, t)
+             : launch(lc, k_op_rows<OP_NT, false, GX_ROWS>, gr, bl, t);
 }
 
 }  // namespace moe

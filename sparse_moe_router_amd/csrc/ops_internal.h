@@ -22,18 +22,19 @@ struct Groups {
   const int32_t* perm;     // NULL: row p of x
 };
 
-// First row and end of group e, limited to [0, rows]; empty when the end is not above the start.
-__device__ __forceinline__ void group_range(const Groups& g, int e, int64_t* lo, int64_t* hi) {
-  if (!g.offsets) {
-    *lo = 0;
-    *hi = g.rows;
-    return;
-  }
+// Rows lo <= p < hi.
+struct Range {
+  int64_t lo, hi;
+  __device__ __forceinline__ int64_t size() const { return hi - lo; }
+};
+
+// The rows of group e, limited to [0, rows]; empty when the end is not above the start.
+__device__ __forceinline__ Range group_range(const Groups& g, int e) {
+  if (!g.offsets) return Range{0, g.rows};
   int64_t a = g.offsets[e], b = g.offsets[e + 1];
   a = a < 0 ? 0 : a > g.rows ? g.rows : a;
   b = b < a ? a : b > g.rows ? g.rows : b;
-  *lo = a;
-  *hi = b;
+  return Range{a, b};
 }
 
 // Row of x that row p of the grouped order reads; -1: none (a row of zeros).

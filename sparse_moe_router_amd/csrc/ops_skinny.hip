@@ -130,12 +130,11 @@ __global__ __launch_bounds__(64 * SW) void k_op_skinny(SkinnyArgs p) {
       e += __builtin_popcountll(__ballot(i < g.E && g.offsets[i + 1] <= row));
     e = __builtin_amdgcn_readfirstlane(e);
     if (e >= g.E) return;
-    int64_t lo, hi;
-    group_range(g, e, &lo, &hi);
-    if (lo != row) return;
+    if (group_range(g, e).lo != row) return;
   }
-  int64_t lo, hi;
-  group_range(g, e, &lo, &hi);
+  const Range range = group_range(g, e);
+  int64_t lo = range.lo;
+  const int64_t hi = range.hi;
   while (lo < hi) {
     const int rows = (int)(hi - lo < 64 ? hi - lo : 64);
     if (rows <= 16)
