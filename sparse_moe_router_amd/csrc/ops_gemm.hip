@@ -26,7 +26,6 @@ namespace {
 
 constexpr int TB = kOpTile;  // tile edge
 constexpr int HU = 1024;     // 16-byte units of a half-tile stage: 128 rows x 128 bytes, or 64 x 256 (16 KB)
-constexpr int SG = 4;        // row tiles of a block of units
 constexpr int GI = 8192;     // rows of x whose indexes the weight gradient holds in LDS at a time
 
 typedef __attribute__((__vector_size__(4 * sizeof(int16_t)))) int16_t i16x4_t;
@@ -93,61 +92,105 @@ __device__ __forceinline__ void bar() {
   asm volatile("" ::: "memory");
 }
 
-// The row tile and panel of workgroup (xcd, local): group, first row, rows.  A
-// group of c rows has ceil(c / 256) tiles, all of 256 rows but the last; the
-// units (tile, panel), panels of a tile in a row, are cut into eight equal
-// runs, one for each XCD.  Lane l scans the groups [l * per, (l + 1) * per);
-// every wave does the same scan.
+// The row tile and panel of a workgroup: group, first row, rows.  A group of c
+// rows has ceil(c / 256) tiles, all of 256 rows but the last.
 struct RowTile {
   int e;  // -1: none
   int64_t p0;
   int rows;
   int panel;
 };
-__device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan) {
-  const int lane = threadIdx.x & 63;
-  int e = 0;
-  int64_t lo = 0, c = g.rows, i;
-  int64_t mine = 0, incl = 0, total;
-  const int per = (g.E + 63) / 64;
-  if (!g.offsets) {
-    total = (c + TB - 1) / TB;
-  } else {
-    for (int j = 0; j < per; ++j) {
-      const int ge = lane * per + j;
-      if (ge < g.E) mine += (group_range(g, ge).size() + TB - 1) / TB;
-    }
-    incl = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += o;
-    }
-    total = __shfl(incl, 63, 64);
-  }
+
+// One group: the units (tile, panel) are cut into eight equal runs, one for
+// each XCD, and within a run into blocks of four tiles, panel by panel: the 32
+// workgroups that an XCD runs at a time then read about as many tiles' rows as
+// panels' weights (int8 4096 x 8192 x 4096: 126 -> 119 us).
+__device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int64_t local, int npan) {
+  constexpr int SG = 4;
+  const int64_t total = (g.rows + TB - 1) / TB;
   const int64_t run = (total * npan + 7) / 8, unit = xcd * run + local;
   if (local >= run || unit >= total * npan) return RowTile{-1, 0, 0, 0};
-  // within the run, blocks of SG tiles, panel by panel: the 32 workgroups that an XCD runs at a time
-  // then read about as many tiles' rows as panels' weights
   const int64_t sg = unit / (SG * npan), sr = unit - sg * SG * npan;
   const int64_t height = total - sg * SG < SG ? total - sg * SG : SG;
-  const int64_t t = sg * SG + sr % height;
-  i = t;
-  if (g.offsets) {
-    const int src = __builtin_ctzll(__ballot(incl > t));
-    i -= __shfl(incl - mine, src, 64);
-    for (int j = 0; j < per; ++j) {
-      e = src * per + j;
-      const Range r = group_range(g, e);  // the unit exists, so a group below E holds it
-      lo = r.lo;
-      c = r.size();
-      const int64_t n = (c + TB - 1) / TB;
-      if (i < n) break;
-      i -= n;
-    }
+  const int64_t p0 = (sg * SG + sr % height) * TB;
+  return RowTile{0, p0, (int)(g.rows - p0 < TB ? g.rows - p0 : TB), (int)(sr / height)};
+}
+
+// Groups: the tiles in three classes, the tallest first, so that the short
+// ones fill the end of the launch; of each class, in group order, one eighth
+// goes to each XCD: an expert's tiles and a tile's panels then share its
+// weights and rows in one L2, and the XCDs stream from distant experts.
+// Against tiles dealt to the XCDs one by one, and against one run for each XCD
+// in group order: 8192 tokens x 2 over 16 experts 122, 136 and 148 us; 4096 x
+// 8 over 256 experts 241, 304, 241; 2501 x 4 over 60 skewed ones 5x, 52, 60.
+// With fewer than 64 tiles single panels are dealt out.
+// Lane l scans the groups [l * per, (l + 1) * per); every wave does the same scan.
+constexpr int kDealTiles = 64;
+__device__ __forceinline__ int tile_class(int rest) { return rest > 192 ? 0 : rest > 64 ? 1 : 2; }
+__device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan) {
+  if (!g.offsets) return find_tile_dense(g, xcd, local, npan);
+  const int lane = threadIdx.x & 63, per = (g.E + 63) / 64;
+  // tiles of this lane's groups in each class: bits 0..31, 32..47, 48..63
+  uint64_t mine = 0;
+  for (int j = 0; j < per; ++j) {
+    const int e = lane * per + j;
+    if (e >= g.E) break;
+    const int64_t c = group_range(g, e).size();
+    mine += (uint64_t)(c / TB);
+    const int rest = (int)(c % TB);
+    if (rest > 0) mine += (uint64_t)1 << (tile_class(rest) == 0 ? 0 : 16 + 16 * tile_class(rest));
   }
-  const int64_t p0 = lo + i * TB;
-  return RowTile{e, p0, (int)(c - i * TB < TB ? c - i * TB : TB), (int)(sr / height)};
+  uint64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t o = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += o;
+  }
+  const uint64_t all = __shfl(incl, 63, 64);
+  const int64_t n0 = (uint32_t)all, n1 = (all >> 32) & 0xFFFF, total = n0 + n1 + (int64_t)(all >> 48);
+  const int64_t n2 = (int64_t)(all >> 48);
+  int64_t i;  // place in the class
+  int cl, panel;
+  if (total >= kDealTiles) {
+    i = local / npan;
+    panel = (int)(local % npan);
+    const int64_t a0 = n0 * xcd / 8, m0 = n0 * (xcd + 1) / 8 - a0;
+    const int64_t a1 = n1 * xcd / 8, m1 = n1 * (xcd + 1) / 8 - a1;
+    const int64_t a2 = n2 * xcd / 8, m2 = n2 * (xcd + 1) / 8 - a2;
+    if (i < m0) {
+      cl = 0, i += a0;
+    } else if (i < m0 + m1) {
+      cl = 1, i += a1 - m0;
+    } else if (i < m0 + m1 + m2) {
+      cl = 2, i += a2 - m0 - m1;
+    } else {
+      return RowTile{-1, 0, 0, 0};
+    }
+  } else {
+    i = (local * 8 + xcd) / npan;
+    panel = (int)((local * 8 + xcd) % npan);
+    if (i >= total) return RowTile{-1, 0, 0, 0};
+    cl = i < n0 ? 0 : i < n0 + n1 ? 1 : 2;
+    i -= cl == 0 ? 0 : cl == 1 ? n0 : n0 + n1;
+  }
+  const int shift = cl == 0 ? 0 : 16 + 16 * cl;
+  const uint64_t mask = cl == 0 ? 0xFFFFFFFFu : 0xFFFFu;
+  const int src = __builtin_ctzll(__ballot((int64_t)((incl >> shift) & mask) > i));
+  i -= (int64_t)((__shfl(incl - mine, src, 64) >> shift) & mask);
+  for (int j = 0; j < per; ++j) {
+    const int e = src * per + j;
+    if (e >= g.E) break;  // not reached: the lane's count says that a group below holds the tile
+    const Range r = group_range(g, e);
+    const int64_t full = r.size() / TB;
+    const int rest = (int)(r.size() % TB);
+    const int64_t here = (cl == 0 ? full : 0) + (rest > 0 && tile_class(rest) == cl);
+    if (i < here) {
+      const int64_t k = cl == 0 ? i : full;  // the tile's place in its group
+      return RowTile{e, r.lo + k * TB, k < full ? TB : rest, panel};
+    }
+    i -= here;
+  }
+  return RowTile{-1, 0, 0, 0};
 }
 
 // One output tile, eight waves: wm = wave / 4, wn = wave % 4.  The tile's rows
@@ -577,26 +620,30 @@ __global__ __launch_bounds__(512, 1) void k_op_rows(TileArgs p) {
     tile_product<KIND, I8, 1, 0, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
 }
 
-// Weight gradients (TN): a workgroup per expert and 256 x 256 tile of dw.
+// Weight gradients (TN): a workgroup per expert and 256 x 256 tile of dw, in
+// eight equal runs, one for each XCD: an expert's tiles share dy and x in one
+// L2.
 template <int GX>
 __global__ __launch_bounds__(512, 1) void k_op_wgrad(TileArgs p) {
   __shared__ u32x4_t lds[8 * HU];
   __shared__ int32_t gidx[GX == GX_ROWS ? 1 : GI];  // 32 KB
-  // an expert's tiles follow one another on one XCD: they share dy and x
   const int per = p.nrow * p.npan;
   const int run = (p.g.E * per + 7) / 8, unit = (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3);
   if (unit >= p.g.E * per) return;
   const int e = unit / per, tile = unit % per;
   const Range r = group_range(p.g, e);
-  tile_product<OP_TN, false, 2, 2, GX>(p, e, uniform64(r.lo), 0, uniform64(r.size()), tile / p.npan, tile % p.npan, lds, gidx);
+  tile_product<OP_TN, false, 2, 2, GX>(p, e, uniform64(r.lo), 0, uniform64(r.size()), tile / p.npan, tile % p.npan, lds,
+                                       gidx);
 }
 
 }  // namespace
 
 int64_t op_tile_units(OpKind kind, const Groups& g) {
   const int64_t pn = (g.N + TB - 1) / TB, pk = (g.K + TB - 1) / TB;
-  const int64_t tiles = kind == OP_TN ? g.E * pn : (g.rows + TB - 1) / TB + (g.offsets ? (g.E < g.rows ? g.E : g.rows) : 0);
-  return (tiles * (kind == OP_NT ? pn : pk) + 7) / 8 * 8;
+  if (kind == OP_TN) return (g.E * pn * pk + 7) / 8 * 8;
+  const int64_t npan = kind == OP_NT ? pn : pk;
+  const int64_t tiles = (g.rows + TB - 1) / TB + (g.offsets ? (g.E < g.rows ? g.E : g.rows) : 0);
+  return g.offsets && tiles >= kDealTiles ? ((tiles + 7) / 8 + 3) * 8 * npan : (tiles * npan + 7) / 8 * 8;
 }
 
 hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, const void* b, const Scales& sc,
