@@ -100,8 +100,8 @@ moe_status_t moe_quantize_i8(int64_t rows, int32_t K, int64_t ldx, const void* x
  *   y        bf16 or fp32 [rows][ldy]
  * Shapes: N a multiple of 8, K a multiple of 16, ldx a multiple of 8 (codes:
  * 16), ldy a multiple of 8, the other limits as for the bf16 products.
- * workspace: moe_matmul_i8_workspace_size bytes (0 for codes), 256-byte
- * aligned; calls sharing one must be ordered. */
+ * workspace: moe_matmul_i8_workspace_size bytes (0 for a few bf16 rows, and not
+ * used with codes), 256-byte aligned; calls sharing one must be ordered. */
 size_t moe_matmul_i8_workspace_size(const moe_groups_t* g);
 moe_status_t moe_matmul_i8(const moe_groups_t* g, const void* x, const float* x_scale, const void* w,
                            const float* w_scale, const float* bias, void* y, moe_dtype_t y_type, void* workspace,

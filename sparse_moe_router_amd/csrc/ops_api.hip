@@ -18,6 +18,7 @@ constexpr int64_t kMaxLd = 1 << 20;  // 256 rows stay within the range of a buff
 // The matrix-vector kernel takes calls that average at most this many rows an
 // expert, the matrix-matrix kernel the others.
 constexpr int kSkinnyRows = 16;
+constexpr int kInsideElems = 16384;
 
 // bytes from the first to the last element of a [rows][cols] buffer of row stride ld
 size_t extent(int64_t rows, int64_t ld, int64_t cols, int es) {
@@ -68,10 +69,14 @@ bool skinny(const Groups& g) {
   return g.rows <= (int64_t)kSkinnyRows * g.E && g.N * groups < ((int64_t)1 << 28);
 }
 
+// bf16 tokens for int8 weights that the matrix-vector kernel quantises itself,
+// every workgroup for its own use, instead of a launch before it.
+bool quantize_inside(const Groups& g) { return skinny(g) && g.x_rows <= 4 && g.x_rows * g.K <= kInsideElems; }
+
 // The forward product of either kind on checked arguments.
 moe_status_t run_forward(bool i8, const Groups& g, const void* x, const void* w, const Scales& sc, void* y, bool fp32,
                          hipStream_t s) {
-  const hipError_t e = skinny(g) ? launch_op_skinny(i8, g, x, w, sc, y, fp32, s)
+  const hipError_t e = skinny(g) ? launch_op_skinny(i8, false, g, x, w, sc, y, fp32, s)
                                  : launch_op_tile(OP_NT, i8, g, x, w, sc, y, fp32, s);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }
@@ -239,7 +244,7 @@ moe_status_t moe_quantize_i8(int64_t rows, int32_t K, int64_t ldx, const void* x
 
 size_t moe_matmul_i8_workspace_size(const moe_groups_t* d) {
   Checked c;
-  if (check_groups(d, 16, 8, &c) != MOE_OK || check_x_rows(d) != MOE_OK) return 0;
+  if (check_groups(d, 16, 8, &c) != MOE_OK || check_x_rows(d) != MOE_OK || quantize_inside(c.g)) return 0;
   return codes_bytes(d) + (((size_t)d->x_rows * 4 + 255) & ~(size_t)255);
 }
 
@@ -273,6 +278,10 @@ moe_status_t moe_matmul_i8(const moe_groups_t* d, const void* x, const float* x_
     r.output(workspace, need);
   }
   if (!r.disjoint()) return MOE_ERR_INVALID_ARG;
+  if (!x_scale && quantize_inside(c.g)) {
+    const hipError_t e = launch_op_skinny(true, true, c.g, x, w, sc, y, f32, stream);
+    return e == hipSuccess ? MOE_OK : hip_fail(e);
+  }
   if (!x_scale) {
     float* scale = (float*)((char*)workspace + codes_bytes(d));
     if (d->x_rows > 0) {

@@ -58,8 +58,9 @@ enum OpKind { OP_NT = 0, OP_NN = 1, OP_TN = 2 };
 // Matrix-matrix kernels: y = x W^T, dx = dy W, dw = dy^T x.  i8: y from codes.
 hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, const void* b, const Scales& sc,
                           void* out, bool fp32, hipStream_t s);
-// Matrix-vector kernel for few rows an expert: y = x W^T.
-hipError_t launch_op_skinny(bool i8, const Groups& g, const void* x, const void* w, const Scales& sc, void* y,
+// Matrix-vector kernel for few rows an expert: y = x W^T.  quantize: x is bf16,
+// w int8, and every workgroup quantises its rows itself.
+hipError_t launch_op_skinny(bool i8, bool quantize, const Groups& g, const void* x, const void* w, const Scales& sc, void* y,
                             bool fp32, hipStream_t s);
 hipError_t launch_quantize_i8(int64_t rows, int K, int64_t ldx, const uint16_t* x, int8_t* codes, float* scale,
                               hipStream_t s);

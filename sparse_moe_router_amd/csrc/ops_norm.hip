@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "ops_internal.h"
+#include "quantize8.h"
 
 namespace moe {
 namespace {
@@ -237,24 +238,46 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
   for (int j = 0; j < CPT; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) aw[j][i] = an[j][i] = 0.0f;
-  for (int64_t row = (int64_t)blockIdx.x * R + (WPR == 1 ? wave : 0); row < p.rows; row += (int64_t)gridDim.x * R) {
+  struct Row {
     Raw8<S32> v[CPT], d[CPT];
     Raw8<false> dh[CPT], y[CPT], gt[CPT];
+  };
+  auto load = [&](Row& q, int64_t row) {
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
       const int c = t + 64 * WPR * j;
-      if (c < nc) {
+      if (c < nc && row < p.rows) {
         if (next) {
-          v[j].load(p.out.data, row * p.out.ld + 8 * c);
-          dh[j].load(p.d_h.data, row * p.d_h.ld + 8 * c);
+          q.v[j].load(p.out.data, row * p.out.ld + 8 * c);
+          q.dh[j].load(p.d_h.data, row * p.d_h.ld + 8 * c);
         }
-        if (p.d_out.data) d[j].load(p.d_out.data, row * p.d_out.ld + 8 * c);
+        if (p.d_out.data) q.d[j].load(p.d_out.data, row * p.d_out.ld + 8 * c);
         if (MERGE) {
-          y[j].load(p.y.data, row * p.y.ld + 8 * c);
-          if (p.gate_mode == MOE_GATE_ELEMENT) gt[j].load(p.gate.data, row * p.gate.ld + 8 * c);
+          q.y[j].load(p.y.data, row * p.y.ld + 8 * c);
+          if (p.gate_mode == MOE_GATE_ELEMENT) q.gt[j].load(p.gate.data, row * p.gate.ld + 8 * c);
         }
       }
     }
+  };
+  // the next row's loads are on their way while this one's sums are taken, where a thread's part
+  // of a row is one chunk (two rows of two would not fit the registers)
+  constexpr bool AHEAD = CPT == 1;
+  const int64_t stride = (int64_t)gridDim.x * R, row0 = (int64_t)blockIdx.x * R + (WPR == 1 ? wave : 0);
+  Row ahead;
+  if (AHEAD) load(ahead, row0);
+  for (int64_t row = row0; row < p.rows; row += stride) {
+    Row cur;
+    if (AHEAD) {
+      cur = ahead;
+      load(ahead, row + stride);
+    } else {
+      load(cur, row);
+    }
+    const Raw8<S32>(&v)[CPT] = cur.v;
+    const Raw8<S32>(&d)[CPT] = cur.d;
+    const Raw8<false>(&dh)[CPT] = cur.dh;
+    const Raw8<false>(&y)[CPT] = cur.y;
+    const Raw8<false>(&gt)[CPT] = cur.gt;
     // sums: v^2, d_h w' v, y^2
     float s1[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -397,33 +420,40 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
   }
 }
 
-// d_weight / d_next_weight: sums over the workgroups' parts.  A workgroup takes
-// 16 columns; its 16 groups of 16 threads take every 16th part each.
-__global__ __launch_bounds__(256) void k_norm_reduce(const float* part, int groups, int H, float* d0, float* d1) {
-  __shared__ float lds[16][17];
+// d_weight / d_next_weight: sums over the workgroups' parts, in a fixed order.
+// A workgroup takes 64 columns; its 32 groups of 16 threads take every 32nd
+// part each, 16 bytes a thread, eight loads in flight.
+__global__ __launch_bounds__(512) void k_norm_reduce(const float* part, int groups, int H, float* d0, float* d1) {
+  __shared__ f32x4_t lds[32][16];
   const int k = blockIdx.y;
   float* dst = k ? d1 : d0;
   if (!dst) return;
   const int cx = threadIdx.x & 15, gy = threadIdx.x >> 4;
-  const int col = blockIdx.x * 16 + cx;
-  float s = 0.0f;
-  if (col < H)
-    for (int g = gy; g < groups; g += 16) s += part[((int64_t)g * 2 + k) * H + col];
+  const int col = blockIdx.x * 64 + 4 * cx;  // H is a multiple of 8
+  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (col < H) {
+    for (int g0 = gy; g0 < groups; g0 += 32 * 8) {
+      f32x4_t v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int g = g0 + 32 * u;
+        v[u] = g < groups ? *(const f32x4_t*)(part + ((int64_t)g * 2 + k) * H + col) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+  }
   lds[gy][cx] = s;
   __syncthreads();
   if (gy == 0 && col < H) {
-    float r = 0.0f;
+    f32x4_t r = lds[0][cx];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r += lds[i][cx];
-    dst[col] = r;
+    for (int i = 1; i < 32; ++i) r += lds[i][cx];
+    *(f32x4_t*)(dst + col) = r;
   }
 }
 
-// codes = rint(127 x / max|x|), half to even.  127 x is exact in fp32 (15
-// significant bits), and the correctly rounded quotient lies on the same side
-// of every border n + 1/2 as the exact one: both are dyadic with the border
-// itself representable, and a quotient that is not a border differs from it by
-// at least 2^-17, more than the half ulp 2^-18 of values up to 127.
+// Codes and scales of token rows (quantize8).
 template <int WPR, int CPT>
 __global__ __launch_bounds__(64 * kWaves<WPR>) void k_quantize(int64_t rows, int K, int64_t ldx, const uint16_t* x,
                                                                int8_t* codes, float* scale) {
@@ -432,18 +462,14 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_quantize(int64_t rows, int
   const int nc = K / 8;
   for (int64_t row = first_row<WPR>(); row < rows; row += row_stride<WPR>()) {
     u32x4_t v[CPT];
-    uint32_t m = 0;  // the largest magnitude's bits; infinities and NaN lie above every finite value's
+    uint32_t m = 0;  // the largest magnitude's bits
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
       const int c = t + 64 * WPR * j;
       if (c < nc) {
         v[j] = *(const u32x4_t*)(x + row * ldx + 8 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t lo = (v[j][i] << 16) & 0x7FFFFFFFu, hi = v[j][i] & 0x7FFF0000u;
-          m = m > lo ? m : lo;
-          m = m > hi ? m : hi;
-        }
+        const uint32_t o = max_magnitude(v[j]);
+        m = m > o ? m : o;
       }
     }
 #pragma unroll
@@ -460,23 +486,10 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_quantize(int64_t rows, int
     }
     const float big = __uint_as_float(m);
     if (t == 0) scale[row] = big / 127.0f;
-    const float down = big > 0x1p120f ? 0x1p-8f : 1.0f;  // keeps 127 x finite; exact where a code is not 0
-    const bool plain = m > 0 && m < 0x7F800000u;
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
       const int c = t + 64 * WPR * j;
-      if (c < nc) {
-        uint32_t w[2] = {0, 0};
-        if (plain) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float f = i & 1 ? bf16_hi(v[j][i >> 1]) : bf16_lo(v[j][i >> 1]);
-            const int q = (int)rintf(127.0f * (f * down) / (big * down));
-            w[i >> 2] |= ((uint32_t)q & 0xFFu) << (8 * (i & 3));
-          }
-        }
-        *(uint64_t*)(codes + row * K + 8 * c) = (uint64_t)w[1] << 32 | w[0];
-      }
+      if (c < nc) *(uint64_t*)(codes + row * K + 8 * c) = quantize8(v[j], big);
     }
   }
 }
@@ -551,7 +564,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, bool merge, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   const Launch lc{s, nullptr, nullptr};
-  return launch(lc, k_norm_reduce, dim3((a.H + 15) / 16, 2), dim3(256), (const float*)a.part, groups, a.H,
+  return launch(lc, k_norm_reduce, dim3((a.H + 63) / 64, 2), dim3(512), (const float*)a.part, groups, a.H,
                 merge ? a.d_weight : nullptr, merge ? a.d_next_weight : a.d_weight);
 }
 

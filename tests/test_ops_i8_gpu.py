@@ -82,7 +82,7 @@ def test_quantize_nonfinite_rows():
     assert torch.isfinite(y[~bad.cuda()]).all()
 
 
-DENSE = [(1, 8, 16), (1, 4096, 2048), (2, 136, 528), (16, 264, 272), (17, 72, 64), (33, 1000, 144), (64, 40, 16384),
+DENSE = [(3, 24, 4112), (4, 72, 2064), (2, 40, 8192), (1, 16, 16384), (1, 8, 16), (1, 4096, 2048), (2, 136, 528), (16, 264, 272), (17, 72, 64), (33, 1000, 144), (64, 40, 16384),
          (65, 520, 1040), (257, 264, 2064), (600, 328, 4112)]
 
 
@@ -198,4 +198,4 @@ def test_no_rows_and_refusals():
     with pytest.raises(ValueError, match="out"):
         ops.matmul_i8(x, w, ws, out=torch.empty(5, 32, dtype=BF16, device="cuda"))
     with pytest.raises(ops.MoeError, match="WORKSPACE_TOO_SMALL"):
-        ops.matmul_i8(x, w, ws, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        ops.matmul_i8(randn(1, 40, 64).cuda(), w, ws, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
