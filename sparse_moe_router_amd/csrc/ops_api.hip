@@ -15,9 +15,6 @@ constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 constexpr int kMaxN = 1 << 20, kMaxK = 16384;
 constexpr int64_t kMaxLd = 1 << 20;  // 256 rows stay within the range of a buffer descriptor
 
-// The matrix-vector kernel takes calls that average at most this many rows an
-// expert, the matrix-matrix kernel the others.
-constexpr int kSkinnyRows = 16;
 constexpr int kInsideElems = 16384;
 
 // bytes from the first to the last element of a [rows][cols] buffer of row stride ld
@@ -63,20 +60,29 @@ void group_regions(Regions* r, const Groups& g) {
 
 bool check_type(moe_dtype_t t) { return t == MOE_DT_BF16 || t == MOE_DT_FP32; }
 
-bool skinny(const Groups& g) {
-  const int64_t groups = g.rows < g.E ? g.rows : g.E;
-  // 16 threads a weight row and group of its launch: below 2^32 in all
-  return g.rows <= (int64_t)kSkinnyRows * g.E && g.N * groups < ((int64_t)1 << 28);
+// Matrix-vector or matrix-matrix kernel for y = x W^T.  The latter takes the
+// time of one tile's reduction however few tiles there are: measured 5.7 us +
+// 2.9 ns a byte of a weight row.  The former takes 3 us + the touched weights
+// (at most min(E, rows) experts') at 3.9 TB/s, by 1/43 longer for each row of a
+// group.  It runs where that is less, and with a margin for short rows, on
+// which its rate falls.  Both sides, us (matrix-vector / matrix-matrix): rows of
+// 4 KB, N 4096, one expert: 8 rows 6.5 / 16.2, 64 rows 12.1 / 16.8, 128 rows
+// 22.8 / 21.0; N 1024, top-8 of 256: 1 token 8.9 / 19.0, 2 tokens 18.3 / 19.3,
+// 4 tokens 34.9 / 24.1; N 8192 of 16 KB: 16 rows 38.5 / 53.0, 64 rows 82 / 55;
+// N 2048 of 1 KB, top-8: 1 token 10.8 / 9.6.
+bool skinny(const Groups& g, int es) {
+  const int64_t groups = g.rows < g.E ? g.rows : g.E, row_bytes = (int64_t)g.K * es;
+  return g.N * (43 * groups + g.rows) < 43 * (12000 + 4000000 / row_bytes);
 }
 
 // bf16 tokens for int8 weights that the matrix-vector kernel quantises itself,
 // every workgroup for its own use, instead of a launch before it.
-bool quantize_inside(const Groups& g) { return skinny(g) && g.x_rows <= 4 && g.x_rows * g.K <= kInsideElems; }
+bool quantize_inside(const Groups& g) { return skinny(g, 1) && g.x_rows <= 4 && g.x_rows * g.K <= kInsideElems; }
 
 // The forward product of either kind on checked arguments.
 moe_status_t run_forward(bool i8, const Groups& g, const void* x, const void* w, const Scales& sc, void* y, bool fp32,
                          hipStream_t s) {
-  const hipError_t e = skinny(g) ? launch_op_skinny(i8, false, g, x, w, sc, y, fp32, s)
+  const hipError_t e = skinny(g, i8 ? 1 : 2) ? launch_op_skinny(i8, false, g, x, w, sc, y, fp32, s)
                                  : launch_op_tile(OP_NT, i8, g, x, w, sc, y, fp32, s);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }

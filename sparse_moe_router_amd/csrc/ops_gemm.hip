@@ -39,6 +39,7 @@ struct TileArgs {
   int fp32;
   int npan;    // tiles along the second output dimension
   int nrow;    // TN: tiles along n
+  int stream;  // TN: results are written past the caches
 };
 
 // Transfers go through range-checked buffer descriptors: a lane whose offset
@@ -67,6 +68,15 @@ __device__ __forceinline__ window_t window(const char* base, int64_t bytes) {
 // lane i of the wave writes the 16 bytes at offset off + step_off of the window to LDS address dst + 16 i
 __device__ __forceinline__ void dma(window_t w, uint32_t off, int step_off, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst), "v"(off),
+               "s"(w.d), "s"(step_off)
+               : "memory");
+}
+// the same with the non-temporal hint: weights that one workgroup alone reads leave the caches to the
+// rows (4096 tokens x 8 over 256 experts 249 -> 226 us; weights that several tiles read lose by it,
+// and so do rows off the cache lines, whose lines two steps share: 2501 x 4 over 60 skewed experts
+// of 2832-byte rows 53 -> 83 us)
+__device__ __forceinline__ void dma_once(window_t w, uint32_t off, int step_off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(dst), "v"(off),
                "s"(w.d), "s"(step_off)
                : "memory");
 }
@@ -99,21 +109,22 @@ struct RowTile {
   int64_t p0;
   int rows;
   int panel;
+  int once;  // the group's only tile, of weight rows in whole cache lines
 };
 
 // One group: the units (tile, panel) are cut into eight equal runs, one for
 // each XCD, and within a run into blocks of four tiles, panel by panel: the 32
 // workgroups that an XCD runs at a time then read about as many tiles' rows as
 // panels' weights (int8 4096 x 8192 x 4096: 126 -> 119 us).
-__device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int64_t local, int npan) {
+__device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int64_t local, int npan, bool aligned) {
   constexpr int SG = 4;
   const int64_t total = (g.rows + TB - 1) / TB;
   const int64_t run = (total * npan + 7) / 8, unit = xcd * run + local;
-  if (local >= run || unit >= total * npan) return RowTile{-1, 0, 0, 0};
+  if (local >= run || unit >= total * npan) return RowTile{-1, 0, 0, 0, 0};
   const int64_t sg = unit / (SG * npan), sr = unit - sg * SG * npan;
   const int64_t height = total - sg * SG < SG ? total - sg * SG : SG;
   const int64_t p0 = (sg * SG + sr % height) * TB;
-  return RowTile{0, p0, (int)(g.rows - p0 < TB ? g.rows - p0 : TB), (int)(sr / height)};
+  return RowTile{0, p0, (int)(g.rows - p0 < TB ? g.rows - p0 : TB), (int)(sr / height), total == 1 && aligned};
 }
 
 // Groups: the tiles in three classes, the tallest first, so that the short
@@ -127,8 +138,8 @@ __device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int
 // Lane l scans the groups [l * per, (l + 1) * per); every wave does the same scan.
 constexpr int kDealTiles = 64;
 __device__ __forceinline__ int tile_class(int rest) { return rest > 192 ? 0 : rest > 64 ? 1 : 2; }
-__device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan) {
-  if (!g.offsets) return find_tile_dense(g, xcd, local, npan);
+__device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan, bool aligned) {
+  if (!g.offsets) return find_tile_dense(g, xcd, local, npan, aligned);
   const int lane = threadIdx.x & 63, per = (g.E + 63) / 64;
   // tiles of this lane's groups in each class: bits 0..31, 32..47, 48..63
   uint64_t mine = 0;
@@ -164,12 +175,12 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
     } else if (i < m0 + m1 + m2) {
       cl = 2, i += a2 - m0 - m1;
     } else {
-      return RowTile{-1, 0, 0, 0};
+      return RowTile{-1, 0, 0, 0, 0};
     }
   } else {
     i = (local * 8 + xcd) / npan;
     panel = (int)((local * 8 + xcd) % npan);
-    if (i >= total) return RowTile{-1, 0, 0, 0};
+    if (i >= total) return RowTile{-1, 0, 0, 0, 0};
     cl = i < n0 ? 0 : i < n0 + n1 ? 1 : 2;
     i -= cl == 0 ? 0 : cl == 1 ? n0 : n0 + n1;
   }
@@ -186,11 +197,11 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
     const int64_t here = (cl == 0 ? full : 0) + (rest > 0 && tile_class(rest) == cl);
     if (i < here) {
       const int64_t k = cl == 0 ? i : full;  // the tile's place in its group
-      return RowTile{e, r.lo + k * TB, k < full ? TB : rest, panel};
+      return RowTile{e, r.lo + k * TB, k < full ? TB : rest, panel, r.size() <= TB && aligned};
     }
     i -= here;
   }
-  return RowTile{-1, 0, 0, 0};
+  return RowTile{-1, 0, 0, 0, 0};
 }
 
 // One output tile, eight waves: wm = wave / 4, wn = wave % 4.  The tile's rows
@@ -218,7 +229,7 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
 // gathered (TN), GX_FAR gathered, by 64-bit addresses.
 enum { GX_ROWS = 0, GX_INDEX = 1, GX_FAR = 2 };
 template <OpKind KIND, bool I8, int RB0, int RB1, int GX>
-__device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p0, int rows, int64_t len, int r0t,
+__device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p0, int rows, int once, int64_t len, int r0t,
                                              int panel, u32x4_t* lds, int32_t* gidx) {
   constexpr bool AT = KIND == OP_TN, BT = KIND != OP_NT;  // operand reduces across its rows
   constexpr int ES = I8 ? 1 : 2;                          // bytes an element
@@ -354,7 +365,11 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     for (int i = 0; i < 2; ++i) {
       const uint32_t dst = lds0 + (sb(j, st) - lds + (wave * 2 + i) * 64) * 16;
       if (!BT) {
-        dma(window(bbase, bbytes), s >= nsteps - 1 && !bend[j][i] ? kOut : boff[j][i], sc * 128, dst);
+        const uint32_t off = s >= nsteps - 1 && !bend[j][i] ? kOut : boff[j][i];
+        if (once)
+          dma_once(window(bbase, bbytes), off, sc * 128, dst);
+        else
+          dma(window(bbase, bbytes), off, sc * 128, dst);
       } else if (KIND == OP_TN && gather) {
         // rows past the end have no index: -1
         const int32_t t = gidx[sc * 64 + (wave * 2 + i) * 4 + (lane >> 4)];
@@ -363,6 +378,8 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           dma64(in ? bbase + (int64_t)t * g.ldx * 2 + boff[j][i] : (const char*)kZero, dst);
         else
           dma(window(bbase, bbytes), in ? (uint32_t)(t * (int)g.ldx * 2) + boff[j][i] : kOut, 0, dst);
+      } else if (KIND == OP_NN && once) {
+        dma_once(step_window(bbase, bstep, s, 2 * g.K), boff[j][i], 0, dst);
       } else {
         dma(step_window(bbase, bstep, s, 2 * g.K), boff[j][i], 0, dst);
       }
@@ -546,6 +563,12 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       }
     }
   }
+  auto put = [&](auto* at, auto value) {
+    if (KIND == OP_TN && p.stream)
+      __builtin_nontemporal_store(value, at);
+    else
+      *at = value;
+  };
   uint16_t* stage = (uint16_t*)(lds + HU) + wave * (32 * 64);  // 4 KB a wave
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -573,7 +596,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           float* orow = (float*)p.out + (row_base + row) * ldo + c0 + l32;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (row < nrows && c0 + col_of(j, wn) + l32 < ncols) orow[col_of(j, wn)] = v[j][r];
+            if (row < nrows && c0 + col_of(j, wn) + l32 < ncols) put(orow + col_of(j, wn), v[j][r]);
         }
       } else {
 #pragma unroll
@@ -590,8 +613,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           const int row = c >> 3, q = c & 7;
           const int grow = row0 + row, col = c0 + col_of(q >> 2, wn) + 8 * (q & 3);
           if (grow < nrows && col < ncols)
-            *(u32x4_t*)((uint16_t*)p.out + (row_base + grow) * ldo + col) =
-                *(const u32x4_t*)(stage + row * 64 + 8 * q);
+            put((u32x4_t*)((uint16_t*)p.out + (row_base + grow) * ldo + col), *(const u32x4_t*)(stage + row * 64 + 8 * q));
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -605,19 +627,19 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
 template <OpKind KIND, bool I8, int GX>
 __global__ __launch_bounds__(512, 1) void k_op_rows(TileArgs p) {
   __shared__ u32x4_t lds[10 * HU];  // 160 KB
-  RowTile tl = find_tile(p.g, blockIdx.x & 7, blockIdx.x >> 3, p.npan);
+  RowTile tl = find_tile(p.g, blockIdx.x & 7, blockIdx.x >> 3, p.npan, p.g.K * (I8 ? 1 : 2) % 128 == 0);
   // the same in every lane, which the compiler cannot see behind the scan
   tl = RowTile{__builtin_amdgcn_readfirstlane(tl.e), uniform64(tl.p0), __builtin_amdgcn_readfirstlane(tl.rows),
-               __builtin_amdgcn_readfirstlane(tl.panel)};
+               __builtin_amdgcn_readfirstlane(tl.panel), __builtin_amdgcn_readfirstlane(tl.once)};
   if (tl.e < 0) return;
   if (tl.rows > 192)
-    tile_product<KIND, I8, 2, 2, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+    tile_product<KIND, I8, 2, 2, GX>(p, tl.e, tl.p0, tl.rows, tl.once, 0, 0, tl.panel, lds, nullptr);
   else if (tl.rows > 128)
-    tile_product<KIND, I8, 2, 1, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+    tile_product<KIND, I8, 2, 1, GX>(p, tl.e, tl.p0, tl.rows, tl.once, 0, 0, tl.panel, lds, nullptr);
   else if (tl.rows > 64)
-    tile_product<KIND, I8, 2, 0, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+    tile_product<KIND, I8, 2, 0, GX>(p, tl.e, tl.p0, tl.rows, tl.once, 0, 0, tl.panel, lds, nullptr);
   else
-    tile_product<KIND, I8, 1, 0, GX>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+    tile_product<KIND, I8, 1, 0, GX>(p, tl.e, tl.p0, tl.rows, tl.once, 0, 0, tl.panel, lds, nullptr);
 }
 
 // Weight gradients (TN): a workgroup per expert and 256 x 256 tile of dw, in
@@ -632,7 +654,7 @@ __global__ __launch_bounds__(512, 1) void k_op_wgrad(TileArgs p) {
   if (unit >= p.g.E * per) return;
   const int e = unit / per, tile = unit % per;
   const Range r = group_range(p.g, e);
-  tile_product<OP_TN, false, 2, 2, GX>(p, e, uniform64(r.lo), 0, uniform64(r.size()), tile / p.npan, tile % p.npan, lds,
+  tile_product<OP_TN, false, 2, 2, GX>(p, e, uniform64(r.lo), 0, 0, uniform64(r.size()), tile / p.npan, tile % p.npan, lds,
                                        gidx);
 }
 
@@ -657,6 +679,9 @@ hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, 
   t.fp32 = fp32;
   t.nrow = (g.N + TB - 1) / TB;
   t.npan = ((kind == OP_NT ? g.N : g.K) + TB - 1) / TB;
+  // weight gradients larger than the last-level cache (256 MB) in whole cache lines: 32768 rows over
+  // 256 experts, 1 GB: 386 -> 355 us
+  t.stream = g.K % 64 == 0 && (int64_t)g.E * g.N * g.K * (fp32 ? 4 : 2) > ((int64_t)1 << 28);
   const unsigned grid = (unsigned)op_tile_units(kind, g);
   const Launch lc{s, nullptr, nullptr};
   // gathered rows past the range of a buffer descriptor are fetched by 64-bit addresses
