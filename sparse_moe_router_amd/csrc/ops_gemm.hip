@@ -137,19 +137,30 @@ __device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int
 // With fewer than 64 tiles single panels are dealt out.
 // Lane l scans the groups [l * per, (l + 1) * per); every wave does the same scan.
 constexpr int kDealTiles = 64;
+// The ranges of groups e .. e + 3, empty from group `end` or E on; their loads are in flight together.
+__device__ __forceinline__ void four_ranges(const Groups& g, int e, int end, Range (&r)[4]) {
+  int32_t v[5];
+  end = end < g.E ? end : g.E;
+#pragma unroll
+  for (int u = 0; u < 5; ++u) v[u] = g.offsets[e + u < end ? e + u : end];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) r[u] = limited(g, v[u], v[u + 1]);
+}
 __device__ __forceinline__ int tile_class(int rest) { return rest > 192 ? 0 : rest > 64 ? 1 : 2; }
 __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan, bool aligned) {
   if (!g.offsets) return find_tile_dense(g, xcd, local, npan, aligned);
   const int lane = threadIdx.x & 63, per = (g.E + 63) / 64;
   // tiles of this lane's groups in each class: bits 0..31, 32..47, 48..63
   uint64_t mine = 0;
-  for (int j = 0; j < per; ++j) {
-    const int e = lane * per + j;
-    if (e >= g.E) break;
-    const int64_t c = group_range(g, e).size();
-    mine += (uint64_t)(c / TB);
-    const int rest = (int)(c % TB);
-    if (rest > 0) mine += (uint64_t)1 << (tile_class(rest) == 0 ? 0 : 16 + 16 * tile_class(rest));
+  for (int j = 0; j < per; j += 4) {
+    Range r[4];
+    four_ranges(g, lane * per + j, lane * per + per, r);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t c = (uint32_t)r[u].size(), rest = c % TB;
+      mine += c / TB;
+      if (rest > 0) mine += (uint64_t)1 << (tile_class(rest) == 0 ? 0 : 16 + 16 * tile_class(rest));
+    }
   }
   uint64_t incl = mine;
 #pragma unroll
@@ -188,20 +199,22 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
   const uint64_t mask = cl == 0 ? 0xFFFFFFFFu : 0xFFFFu;
   const int src = __builtin_ctzll(__ballot((int64_t)((incl >> shift) & mask) > i));
   i -= (int64_t)((__shfl(incl - mine, src, 64) >> shift) & mask);
-  for (int j = 0; j < per; ++j) {
-    const int e = src * per + j;
-    if (e >= g.E) break;  // not reached: the lane's count says that a group below holds the tile
-    const Range r = group_range(g, e);
-    const int64_t full = r.size() / TB;
-    const int rest = (int)(r.size() % TB);
-    const int64_t here = (cl == 0 ? full : 0) + (rest > 0 && tile_class(rest) == cl);
-    if (i < here) {
-      const int64_t k = cl == 0 ? i : full;  // the tile's place in its group
-      return RowTile{e, r.lo + k * TB, k < full ? TB : rest, panel, r.size() <= TB && aligned};
+  for (int j = 0; j < per; j += 4) {
+    Range r[4];
+    four_ranges(g, src * per + j, src * per + per, r);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t full = r[u].size() / TB;
+      const int rest = (int)(r[u].size() % TB);
+      const int64_t here = (cl == 0 ? full : 0) + (rest > 0 && tile_class(rest) == cl);
+      if (i < here) {
+        const int64_t k = cl == 0 ? i : full;  // the tile's place in its group
+        return RowTile{src * per + j + u, r[u].lo + k * TB, k < full ? TB : rest, panel, r[u].size() <= TB && aligned};
+      }
+      i -= here;
     }
-    i -= here;
   }
-  return RowTile{-1, 0, 0, 0, 0};
+  return RowTile{-1, 0, 0, 0, 0};  // not reached: the lane's count says that one of its groups holds the tile
 }
 
 // One output tile, eight waves: wm = wave / 4, wn = wave % 4.  The tile's rows
@@ -228,8 +241,11 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
 // GX: how rows of x are found: GX_ROWS in order (NT: or gathered), GX_INDEX
 // gathered (TN), GX_FAR gathered, by 64-bit addresses.
 enum { GX_ROWS = 0, GX_INDEX = 1, GX_FAR = 2 };
-template <OpKind KIND, bool I8, int RB0, int RB1, int GX>
-__device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p0, int rows, int once, int64_t len, int r0t,
+// ONCE: this tile alone reads its panel of weights, whose rows are whole cache
+// lines (a template, because a branch at each transfer costs tiles bound by
+// the matrix units 6%).
+template <OpKind KIND, bool I8, int RB0, int RB1, int GX, bool ONCE>
+__device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p0, int rows, int64_t len, int r0t,
                                              int panel, u32x4_t* lds, int32_t* gidx) {
   constexpr bool AT = KIND == OP_TN, BT = KIND != OP_NT;  // operand reduces across its rows
   constexpr int ES = I8 ? 1 : 2;                          // bytes an element
@@ -284,7 +300,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   uint32_t aoff[2][RBM], boff[2][2];  // a lane's offsets in its window
   bool aend[2][RBM], bend[2][2];      // along: the lane's chunk lies in the last step
   const char* a64[2][RBM];
-  auto set_sources = [&]() {
+  auto set_steps = [&]() {
     nsteps = (int)((red + BKE - 1) / BKE);
     last = (int)(red - (int64_t)(nsteps - 1) * BKE);
     if (AT) {
@@ -302,6 +318,8 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       bbase = p.b + (gather ? 0 : base * g.ldx * 2);
       bbytes = ((g.x_rows - 1) * g.ldx + g.K) * 2;  // gathered
     }
+  };
+  auto set_a = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -326,6 +344,8 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           aoff[h][i] = col >= g.N ? kOut : (uint32_t)((row * g.ldy + col) * 2);
         }
       }
+  };
+  auto set_b = [&]() {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -366,7 +386,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       const uint32_t dst = lds0 + (sb(j, st) - lds + (wave * 2 + i) * 64) * 16;
       if (!BT) {
         const uint32_t off = s >= nsteps - 1 && !bend[j][i] ? kOut : boff[j][i];
-        if (once)
+        if (ONCE)
           dma_once(window(bbase, bbytes), off, sc * 128, dst);
         else
           dma(window(bbase, bbytes), off, sc * 128, dst);
@@ -378,7 +398,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           dma64(in ? bbase + (int64_t)t * g.ldx * 2 + boff[j][i] : (const char*)kZero, dst);
         else
           dma(window(bbase, bbytes), in ? (uint32_t)(t * (int)g.ldx * 2) + boff[j][i] : kOut, 0, dst);
-      } else if (KIND == OP_NN && once) {
+      } else if (ONCE) {
         dma_once(step_window(bbase, bstep, s, 2 * g.K), boff[j][i], 0, dst);
       } else {
         dma(step_window(bbase, bstep, s, 2 * g.K), boff[j][i], 0, dst);
@@ -463,19 +483,25 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     } else if (done > 0) {
       break;
     }
-    set_sources();
+    set_steps();
+    set_b();
     if constexpr (RB1 > 0) {
       // memory parts: 8, 4, 8 and 4 reads of a block, two transfers a wave in each.  The first column
       // half of a step is read in the last part of the step before.
       constexpr int WB = 6 + RB0 + 2 * RB1, WA = 6 + 2 * RB0 + RB1;
+      // the columns' transfers are on their way while the rows' indexes are read
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         load_b(0, d, d);
-        load_a(0, d, d);
         load_b(1, d, d);
+      }
+      set_a();
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        load_a(0, d, d);
         load_a(1, d, d);
       }
-      wait_vm<WB>();  // first halves of step 0
+      wait_vm<RB0 + 2 * RB1>();  // all columns, first row half of step 0
       bar();
       read_b(0, 0);
       if (wm == 1) bar();
@@ -490,7 +516,11 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           multiply(0, 0);
           read_b(1, u);
           load_a(0, u, s + 2);
-          wait_vm<WA>();  // second row half of this step
+          // second row half of this step; in step 0 fewer transfers come after it than later on
+          if (s == 0)
+            wait_vm<2 + 2 * RB0 + RB1>();
+          else
+            wait_vm<WA>();
           multiply(0, 1);
           read_a(1, u);
           load_b(1, u, s + 2);
@@ -498,7 +528,10 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           multiply(1, 0);
           read_b(0, u ^ 1);
           load_a(1, u, s + 2);
-          wait_vm<WB>();  // first row half of the next step
+          if (s == 0)  // first row half of the next step
+            wait_vm<4 + RB0 + 2 * RB1>();
+          else
+            wait_vm<WB>();
           multiply(1, 1);
         }
       }
@@ -506,11 +539,13 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       constexpr int W = 2 * (ST - 1) + (ST - 2) * (RB0 + 2);
 #pragma unroll
       for (int d = 0; d < ST; ++d) {
-        load_a(0, d, d);
         load_b(0, d, d);
         if (d < ST - 1) load_b(1, d, d);
       }
-      wait_vm<W + RB0 + 2>();  // first halves of step 0
+      set_a();
+#pragma unroll
+      for (int d = 0; d < ST; ++d) load_a(0, d, d);
+      wait_vm<(ST - 1) * RB0>();  // all columns, rows of step 0
       bar();
       read_b(0, 0);
       if (wm == 1) bar();
@@ -521,7 +556,14 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           if (s >= nsteps) break;  // uniform
           read_a(0, u);
           load_b(1, (u + ST - 1) % ST, s + ST - 1);
-          wait_vm<W>();  // second column half of this step, first halves of the next
+          // second column half of this step, first halves of the next; in the first steps fewer
+          // transfers come after those than later on
+          if (s == 0)
+            wait_vm<(ST - 2) * RB0 + 2>();
+          else if (ST == 4 && s == 1)
+            wait_vm<(ST - 2) * RB0 + 6>();
+          else
+            wait_vm<W>();
           multiply(0, 0);
           read_b(1, u);
           read_b(0, (u + 1) % ST);
@@ -632,14 +674,29 @@ __global__ __launch_bounds__(512, 1) void k_op_rows(TileArgs p) {
   tl = RowTile{__builtin_amdgcn_readfirstlane(tl.e), uniform64(tl.p0), __builtin_amdgcn_readfirstlane(tl.rows),
                __builtin_amdgcn_readfirstlane(tl.panel), __builtin_amdgcn_readfirstlane(tl.once)};
   if (tl.e < 0) return;
-  if (tl.rows > 192)
-    tile_product<KIND, I8, 2, 2, GX>(p, tl.e, tl.p0, tl.rows, tl.once, 0, 0, tl.panel, lds, nullptr);
-  else if (tl.rows > 128)
-    tile_product<KIND, I8, 2, 1, GX>(p, tl.e, tl.p0, tl.rows, tl.once, 0, 0, tl.panel, lds, nullptr);
-  else if (tl.rows > 64)
-    tile_product<KIND, I8, 2, 0, GX>(p, tl.e, tl.p0, tl.rows, tl.once, 0, 0, tl.panel, lds, nullptr);
-  else
-    tile_product<KIND, I8, 1, 0, GX>(p, tl.e, tl.p0, tl.rows, tl.once, 0, 0, tl.panel, lds, nullptr);
+  auto run = [&](auto r0, auto r1, auto once) {
+    tile_product<KIND, I8, r0(), r1(), GX, once()>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr);
+  };
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, 1> c1{};
+  constexpr std::integral_constant<int, 2> c2{};
+  if (tl.rows > 192) {
+    run(c2, c2, std::false_type{});
+  } else if (tl.once) {
+    if (tl.rows > 128)
+      run(c2, c1, std::true_type{});
+    else if (tl.rows > 64)
+      run(c2, c0, std::true_type{});
+    else
+      run(c1, c0, std::true_type{});
+  } else {
+    if (tl.rows > 128)
+      run(c2, c1, std::false_type{});
+    else if (tl.rows > 64)
+      run(c2, c0, std::false_type{});
+    else
+      run(c1, c0, std::false_type{});
+  }
 }
 
 // Weight gradients (TN): a workgroup per expert and 256 x 256 tile of dw, in
@@ -654,7 +711,7 @@ __global__ __launch_bounds__(512, 1) void k_op_wgrad(TileArgs p) {
   if (unit >= p.g.E * per) return;
   const int e = unit / per, tile = unit % per;
   const Range r = group_range(p.g, e);
-  tile_product<OP_TN, false, 2, 2, GX>(p, e, uniform64(r.lo), 0, 0, uniform64(r.size()), tile / p.npan, tile % p.npan, lds,
+  tile_product<OP_TN, false, 2, 2, GX, false>(p, e, uniform64(r.lo), 0, uniform64(r.size()), tile / p.npan, tile % p.npan, lds,
                                        gidx);
 }
 

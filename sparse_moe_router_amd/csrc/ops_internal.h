@@ -28,13 +28,16 @@ struct Range {
   __device__ __forceinline__ int64_t size() const { return hi - lo; }
 };
 
-// The rows of group e, limited to [0, rows]; empty when the end is not above the start.
-__device__ __forceinline__ Range group_range(const Groups& g, int e) {
-  if (!g.offsets) return Range{0, g.rows};
-  int64_t a = g.offsets[e], b = g.offsets[e + 1];
+// Rows a <= p < b, limited to [0, rows]; empty when the end is not above the start.
+__device__ __forceinline__ Range limited(const Groups& g, int64_t a, int64_t b) {
   a = a < 0 ? 0 : a > g.rows ? g.rows : a;
   b = b < a ? a : b > g.rows ? g.rows : b;
   return Range{a, b};
+}
+
+// The rows of group e.
+__device__ __forceinline__ Range group_range(const Groups& g, int e) {
+  return g.offsets ? limited(g, g.offsets[e], g.offsets[e + 1]) : Range{0, g.rows};
 }
 
 // Row of x that row p of the grouped order reads; -1: none (a row of zeros).

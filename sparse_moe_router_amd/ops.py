@@ -210,3 +210,25 @@ def block_merge_grad(d_out: Optional[torch.Tensor], y: torch.Tensor, weight: tor
     d_out is the gradient of out (None = 0, with a next norm only).  With next_weight, d_h (bf16) is
     the gradient of h and out the forward call's result."""
     return _call(stream, _ops.block_merge_grad, d_out, y, weight, eps, gate, scale, next_weight, out, d_h, workspace)
+
+
+def block_forward(x: torch.Tensor, router_w: torch.Tensor, expert_w: torch.Tensor, shared_w: Optional[torch.Tensor],
+                  top_k: int, norm_weight: Optional[torch.Tensor], merge_weight: torch.Tensor, eps: float,
+                  gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                  next_weight: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, stream=None, **layer):
+    """A whole MoE block around :func:`sparse_moe_router_amd.forward`: the norm before it, the layer, and
+    the merge after it: ``block_merge(x, forward(h, ...), merge_weight, ...)`` with ``h =
+    block_norm(x, norm_weight)``, or the h that the block before gave (norm_weight is then None).
+
+    x is the residual stream (bf16 or fp32 [tokens, H]); gate, scale and next_weight as in
+    :func:`block_merge`, whose result is returned; other keywords go to ``forward``."""
+    if (h is None) == (norm_weight is None):
+        raise ValueError("either norm_weight or h must be given")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return block_forward(x, router_w, expert_w, shared_w, top_k, norm_weight, merge_weight, eps, gate, scale,
+                                 next_weight, h, **layer)
+    if h is None:
+        h = block_norm(x, norm_weight, eps)
+    y = moe.forward(h, router_w, expert_w, shared_w, top_k, **layer)
+    return block_merge(x, y, merge_weight, eps, gate=gate, scale=scale, next_weight=next_weight)

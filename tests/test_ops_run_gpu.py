@@ -57,6 +57,32 @@ def test_block_from_operators_is_the_fused_layer():
     close(hn, wh, (100 * EPS32 + eps_of(BF16)) * wh.abs())
 
 
+@pytest.mark.parametrize("M", [1, 5, 40, 300])
+def test_block_forward(M):
+    """block_forward is its three parts, for every path of the layer, on the current and on a given
+    stream, and blocks chained through the next norm."""
+    p = layer(M=M)
+    I, E = p["I"], p["E"]
+    packed = torch.cat([p["gu"].reshape(E, -1), p["down"].reshape(E, -1)], 1).contiguous()
+    shared = packed[0].clone()
+    args = (p["router"], packed, shared, p["k"])
+    out, hn = ops.block_forward(p["x"], *args, p["w_in"], p["w_out"], EPS, gate=p["gate"], scale=0.5,
+                                next_weight=p["w_next"])
+    h = ops.block_norm(p["x"], p["w_in"], EPS)
+    want = ops.block_merge(p["x"], moe.forward(h, *args), p["w_out"], EPS, gate=p["gate"], scale=0.5,
+                           next_weight=p["w_next"])
+    assert torch.equal(out, want[0]) and torch.equal(hn, want[1])
+    second = ops.block_forward(out, *args, None, p["w_out"], EPS, h=hn)
+    assert torch.equal(second, ops.block_merge(out, moe.forward(hn, *args), p["w_out"], EPS))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    again = ops.block_forward(p["x"], *args, p["w_in"], p["w_out"], EPS, gate=p["gate"], scale=0.5, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+    with pytest.raises(ValueError, match="norm_weight or h"):
+        ops.block_forward(p["x"], *args, p["w_in"], p["w_out"], EPS, h=h)
+
+
 def test_backward_of_the_block():
     """The gradients of a whole block through the operators' backward calls, against automatic
     differentiation of the block in 64 bits at the same routing."""
