@@ -7,16 +7,26 @@
 //
 // One 8-wave workgroup computes one output tile of up to 256 x 256 over the
 // whole reduction.  Operands travel straight from global memory into LDS
-// rings (global->LDS transfers of 16 bytes a lane, whole cache lines), steps
-// of 64 reduction elements (128 of int8) ahead of the MFMAs.  An operand
-// whose reduction runs along memory (NT both, NN the rows dy) is staged as
-// [256 rows][128 bytes] and read as it lies; one whose reduction runs across
-// rows (NN the weights, TN both) is staged as [64 rows][512 bytes] and read
-// with the transposing LDS read, so no operand is ever transposed in memory.
+// (16 bytes a lane, whole cache lines), steps of 64 reduction elements (128 of
+// int8) ahead of the MFMAs.  An operand whose reduction runs along memory (NT
+// both, NN the rows dy) is staged as [rows][128 bytes] and read as it lies;
+// one whose reduction runs across rows (NN the weights, TN both) is staged as
+// [64 rows][256 bytes] and read with the transposing LDS read, so no operand is
+// ever transposed in memory.
 //
 // Which rows a workgroup has comes from the group offsets on the device: each
 // wave scans them itself (a few loads and a wave scan) instead of waiting for
 // a map made by a launch of its own.
+//
+// Large tiles are bound by the K loop: 16384 rows, 4 experts of 4096 x 4096:
+// 445 us = 1.24 PFLOP/s (NT), 436 us (NN), 416 us = 1.32 (TN); int8 8192^3 2.4 to
+// 2.6 POP/s (against 1.38 PFLOP/s and 2.0 POP/s of library products here).  Its
+// clusters alone, without transfers, run at 1.65 (NT) to 2.0 PFLOP/s (TN), the
+// transfers and LDS reads alone at the time of 1.33 to 1.6: what the two cost
+// each other is what is left.  Many small experts are bound by the stream of
+// the weights (32768 rows over 256 experts of 1024 x 2048: 215 us = 5.6 TB/s),
+// and weight gradients over short groups by their results, which nothing
+// overlaps with the next tile's loads (the same rows: 377 us for 1.07 GB).
 #include <type_traits>
 
 #include "ops_internal.h"
@@ -133,7 +143,7 @@ __device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int
 // weights and rows in one L2, and the XCDs stream from distant experts.
 // Against tiles dealt to the XCDs one by one, and against one run for each XCD
 // in group order: 8192 tokens x 2 over 16 experts 122, 136 and 148 us; 4096 x
-// 8 over 256 experts 241, 304, 241; 2501 x 4 over 60 skewed ones 5x, 52, 60.
+// 8 over 256 experts 241, 304, 241; 2501 x 4 over 60 skewed ones 51, 52, 60.
 // With fewer than 64 tiles single panels are dealt out.
 // Lane l scans the groups [l * per, (l + 1) * per); every wave does the same scan.
 constexpr int kDealTiles = 64;
@@ -611,57 +621,53 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     else
       *at = value;
   };
-  uint16_t* stage = (uint16_t*)(lds + HU) + wave * (32 * 64);  // 4 KB a wave
+  // 32 x 64 results at a time through a part of the LDS of the wave's own, then 16 bytes a lane
+  float* stage = (float*)(lds + HU) + wave * (32 * 64);
+  auto write = [&](auto type) {
+    typedef decltype(type) T;
+    constexpr int EC = 16 / sizeof(T);  // results of a 16-byte chunk
+    T* st = (T*)stage;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int b = 0; b < RBM; ++b) {
-      if (b >= (h ? RB1 : RB0)) continue;
-      const int row0 = (h ? 64 * RB0 : 0) + 32 * ((h ? RB1 : RB0) * wm + b);
-      if (row0 >= nrows) continue;  // uniform
-      float v[2][16];
+      for (int b = 0; b < RBM; ++b) {
+        if (b >= (h ? RB1 : RB0)) continue;
+        const int row0 = (h ? 64 * RB0 : 0) + 32 * ((h ? RB1 : RB0) * wm + b);
+        if (row0 >= nrows) continue;  // uniform
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          if constexpr (I8) {
-            const int row = row0 + 8 * (r >> 2) + 4 * half + (r & 3);
-            v[j][r] = (float)acc[h][b][j][r] * (s_scale[row] * ws[j]) + bi[j];
-          } else {
-            v[j][r] = acc[h][b][j][r];
+          for (int r = 0; r < 16; ++r) {
+            const int row = 8 * (r >> 2) + 4 * half + (r & 3);
+            float v;
+            if constexpr (I8)
+              v = (float)acc[h][b][j][r] * (s_scale[row0 + row] * ws[j]) + bi[j];
+            else
+              v = acc[h][b][j][r];
+            if constexpr (sizeof(T) == 4)
+              st[row * 64 + 32 * j + l32] = v;
+            else
+              st[row * 64 + 32 * j + l32] = (T)f32_to_bf16(v);
           }
-        }
-      if (p.fp32) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int row = row0 + 8 * (r >> 2) + 4 * half + (r & 3);
-          float* orow = (float*)p.out + (row_base + row) * ldo + c0 + l32;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (row < nrows && c0 + col_of(j, wn) + l32 < ncols) put(orow + col_of(j, wn), v[j][r]);
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int row = 8 * (r >> 2) + 4 * half + (r & 3);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) stage[row * 64 + 32 * j + l32] = (uint16_t)f32_to_bf16(v[j][r]);
-        }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
-        for (int c = lane; c < 32 * 8; c += 64) {
-          const int row = c >> 3, q = c & 7;
-          const int grow = row0 + row, col = c0 + col_of(q >> 2, wn) + 8 * (q & 3);
+        for (int c = lane; c < 32 * 64 / EC; c += 64) {
+          const int row = c / (64 / EC), at = c % (64 / EC) * EC;  // column among the wave's 64
+          const int grow = row0 + row, col = c0 + col_of(at >> 5, wn) + (at & 31);
           if (grow < nrows && col < ncols)
-            put((u32x4_t*)((uint16_t*)p.out + (row_base + grow) * ldo + col), *(const u32x4_t*)(stage + row * 64 + 8 * q));
+            put((u32x4_t*)((T*)p.out + (row_base + grow) * ldo + col), *(const u32x4_t*)(st + row * 64 + at));
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
       }
-    }
+  };
+  if (p.fp32)
+    write(0.0f);
+  else
+    write((uint16_t)0);
 }
 
 // Row-tiled products (NT, NN).  Workgroup b runs on XCD b % 8; a row tile's

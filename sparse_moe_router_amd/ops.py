@@ -9,7 +9,9 @@ may be strided (a slice of columns), by a multiple of 16 bytes.  Weights,
 offsets, permutations and per-token vectors are contiguous.  A call runs on the
 current stream of its tensors' device, or on ``stream``; what the caller does
 not pass is allocated there, workspaces among it, so that calls on different
-streams and captured graphs never share one.
+streams and captured graphs never share one; tensors written on other streams
+must be ready on it.  Nothing is recorded for automatic differentiation: the
+gradients are calls of their own.
 
 ``offsets`` (int32 [E+1]) and ``perm`` (int32 [rows]) are the group offsets and
 the permutation that :func:`sparse_moe_router_amd.route` reports.

@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
 
 # counts per expert, N, K: one row; empty first, last and inner groups; sizes around the 16, 32, 64 and
-# 256 row edges; N and K off every tile; more experts than rows; E over the 64 lanes of a wave
+# 256 row edges, and past the 8192 rows whose indexes a weight gradient holds at a time; N and K off every tile; more experts than rows; E over the 64 lanes of a wave
 CASES = {
     "one": ([1], 8, 8),
     "one_expert": ([70], 136, 264),
@@ -18,6 +18,7 @@ CASES = {
     "edges": ([15, 16, 17, 31, 32, 33, 63, 64, 65, 255, 257], 72, 136),
     "tall": ([300, 0, 33, 513, 64], 512, 520),
     "wide_k": ([40, 130], 40, 2056),
+    "long_groups": ([8300, 0, 100, 16500], 72, 72),
     "long_k": ([3, 0, 20], 24, 16384),
     "decode": ([0] * 100 + [1, 0, 1, 1] + [0] * 120 + [1] * 5 + [0] * 27, 256, 2048),
     "small_batch": ([2, 0, 5, 1, 9, 0, 0, 16, 3, 64, 1, 1], 520, 328),
@@ -171,6 +172,23 @@ def test_nonfinite_values_stay_in_their_rows_and_experts(few):
     assert bad.nonzero().flatten().tolist() == [R - 1]
     assert torch.isfinite(dw[0]).all() and not torch.isfinite(dw[1]).any()
     assert torch.isnan(dw[2, 5]).all() and torch.isfinite(dw[2, :5]).all() and torch.isfinite(dw[2, 6:]).all()
+
+
+@pytest.mark.parametrize("rows", [64, 65, 128, 129, 192, 193, 256])
+@pytest.mark.parametrize("K", [8, 64, 72, 128, 136, 256, 320])
+def test_every_tile_height_and_number_of_steps(rows, K):
+    """One group of every height class of tile, reductions of one step up to five, the last one whole or
+    not: every pipeline's beginning and end.  (N is large enough for the matrix-matrix kernel.)"""
+    N = 16400
+    x, w, dy = randn(1, rows, K), randn(2, 1, N, K), randn(3, rows, K)
+    y = ops.grouped_matmul(dev(x), dev(w), None, out_dtype=F32)
+    off = torch.tensor([0, rows])
+    want, tol = grouped_ref(x.to(F8), w, off)
+    close(y, want, tol + EPS32 * want.abs(), "y")
+    wt = w[0, :600].t().contiguous()[None]  # [1, K, 600]: reduction over K again
+    dx = ops.grouped_matmul_grad_input(dev(dy), dev(wt), None, out_dtype=F32)
+    want, tol = grad_input_ref(dy, wt, off)
+    close(dx, want, tol + EPS32 * want.abs(), "dx")
 
 
 def test_no_rows():

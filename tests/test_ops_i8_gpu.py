@@ -105,6 +105,16 @@ def test_matmul(M, N, K, bias, given, dtype):
     close(y, want, tol + eps_of(dtype) * want.abs(), f"{M} {N} {K}")
 
 
+@pytest.mark.parametrize("rows", [64, 65, 128, 129, 192, 193, 256])
+@pytest.mark.parametrize("K", [16, 128, 144, 256, 272, 512, 640])
+def test_every_tile_height_and_number_of_steps(rows, K):
+    N = 16400
+    q, w, ws, xs = codes(1, rows, K), codes(2, N, K), scales(3, N), scales(4, rows)
+    y = ops.matmul_i8(q.cuda(), w.cuda(), ws.cuda(), x_scale=xs.cuda(), out_dtype=F32)
+    want, tol = i8_ref(q.to(F8), xs.to(F8), w, ws)
+    close(y, want, tol + EPS32 * want.abs())
+
+
 def test_extreme_codes_do_not_overflow():
     """The largest sum: K = 16384 products of -128 with -128, 2^28."""
     for M in (1, 300):
