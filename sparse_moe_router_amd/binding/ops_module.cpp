@@ -37,6 +37,7 @@ struct PythonError {};  // the interpreter's error is set already
 
 PyObject* g_raw_stream = nullptr;  // torch._C._cuda_getCurrentRawStream
 PyObject* g_check = nullptr;       // moe._check
+PyObject* g_oom = nullptr;         // torch.OutOfMemoryError
 
 std::string shape_of(const Tensor& t) {
   std::string s = "(";
@@ -202,7 +203,7 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& body) {
     PyErr_SetString(e.type, e.text.c_str());
   } catch (const PythonError&) {
   } catch (const c10::OutOfMemoryError& e) {
-    PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
+    PyErr_SetString(g_oom, e.what_without_backtrace());
   } catch (const c10::Error& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {
@@ -512,5 +513,7 @@ PyMODINIT_FUNC PyInit__ops() {
   if (!g_raw_stream) return nullptr;
   g_check = attribute("sparse_moe_router_amd.moe", "_check");
   if (!g_check) return nullptr;
+  g_oom = attribute("torch", "OutOfMemoryError");
+  if (!g_oom) return nullptr;
   return PyModule_Create(&module);
 }

@@ -226,11 +226,16 @@ def block_forward(x: torch.Tensor, router_w: torch.Tensor, expert_w: torch.Tenso
     :func:`block_merge`, whose result is returned; other keywords go to ``forward``."""
     if (h is None) == (norm_weight is None):
         raise ValueError("either norm_weight or h must be given")
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return block_forward(x, router_w, expert_w, shared_w, top_k, norm_weight, merge_weight, eps, gate, scale,
-                                 next_weight, h, **layer)
-    if h is None:
-        h = block_norm(x, norm_weight, eps)
-    y = moe.forward(h, router_w, expert_w, shared_w, top_k, **layer)
-    return block_merge(x, y, merge_weight, eps, gate=gate, scale=scale, next_weight=next_weight)
+    if stream is None and x.is_cuda:
+        stream = torch.cuda.current_stream(x.device)
+    with torch.cuda.stream(stream):  # and its device
+        if h is None:
+            h = block_norm(x, norm_weight, eps)
+        if "workspace" not in layer:
+            # of the call's own, as every workspace here: captured graphs never share one
+            (M, H), E = h.shape, router_w.shape[0]
+            sizes = expert_w.numel() // (3 * E * H), 0 if shared_w is None else shared_w.numel() // (3 * H)
+            layer["workspace"] = torch.empty(moe.workspace_size(M, H, E, *sizes, top_k, layer.get("flags", 0)),
+                                             dtype=torch.uint8, device=h.device)
+        y = moe.forward(h, router_w, expert_w, shared_w, top_k, **layer)
+        return block_merge(x, y, merge_weight, eps, gate=gate, scale=scale, next_weight=next_weight)

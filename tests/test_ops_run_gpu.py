@@ -217,6 +217,34 @@ def test_two_graphs_replayed_at_once():
             assert all(torch.equal(a, b) for a, b in zip(r, w))
 
 
+def test_two_block_graphs_replayed_at_once():
+    """Two captured blocks (the layer's workspace among their buffers) replayed together."""
+    ps = [layer(M=200, seed=s) for s in (0, 40)]
+    packed = [torch.cat([p["gu"].reshape(p["E"], -1), p["down"].reshape(p["E"], -1)], 1).contiguous() for p in ps]
+
+    def block(i):
+        p = ps[i]
+        return ops.block_forward(p["x"], p["router"], packed[i], None, p["k"], p["w_in"], p["w_out"], EPS,
+                                 gate=p["gate"], next_weight=p["w_next"])
+
+    want = [block(0), block(1)]
+    torch.cuda.synchronize()
+    graphs, res = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res.append(block(i))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(6):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for r, w in zip(res, want):
+            assert torch.equal(r[0], w[0]) and torch.equal(r[1], w[1])
+
+
 def test_other_streams():
     """Calls on a stream given as an argument and on the current one, two at once."""
     ps = [call_inputs(False, s) for s in (0, 70)]
