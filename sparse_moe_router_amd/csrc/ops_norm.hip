@@ -570,7 +570,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, bool merge, hipStream_t s) {
 
 hipError_t launch_quantize_i8(int64_t rows, int K, int64_t ldx, const uint16_t* x, int8_t* codes, float* scale,
                               hipStream_t s) {
-  return with_plan(row_plan(rows, K, 4), [&](auto w, auto c) {
+  return with_plan(row_plan(rows, K, 2), [&](auto w, auto c) {
     constexpr int WPR = w(), CPT = c();
     const unsigned grid = row_grid<WPR>(rows);
     return launch(Launch{s, nullptr, nullptr}, k_quantize<WPR, CPT>, dim3(grid), dim3(64 * kWaves<WPR>), rows, K, ldx,
