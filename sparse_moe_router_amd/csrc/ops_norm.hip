@@ -233,11 +233,33 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
   // block_norm_grad is the "next norm" half alone: out = x, dn = d_h, d_out = d_add
   const bool next = MERGE ? p.d_h.data != nullptr : true;
   const void* wn = MERGE ? p.next_weight : p.weight;
-  float aw[CPT][8], an[CPT][8];
+  // this thread's part of the weight gradients; with four chunks a thread in LDS ([2][H], each thread
+  // its own columns), as the registers do not hold it beside the row
+  constexpr bool LDS_SUMS = WPR == 8 && CPT == 4;
+  extern __shared__ f32x4_t sums[];
+  float aw[LDS_SUMS ? 1 : CPT][8], an[LDS_SUMS ? 1 : CPT][8];
+  auto add = [&](int k, int j, const float(&f)[8]) {
+    if (LDS_SUMS) {
+      f32x4_t* at = sums + (k * p.H + 8 * (t + 64 * WPR * j)) / 4;
+      at[0] += f32x4_t{f[0], f[1], f[2], f[3]};
+      at[1] += f32x4_t{f[4], f[5], f[6], f[7]};
+    } else {
 #pragma unroll
-  for (int j = 0; j < CPT; ++j)
+      for (int i = 0; i < 8; ++i) (k ? an : aw)[LDS_SUMS ? 0 : j][i] += f[i];
+    }
+  };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) aw[j][i] = an[j][i] = 0.0f;
+  for (int j = 0; j < CPT; ++j) {
+    if (LDS_SUMS) {
+      for (int k = 0; k < 2 && t + 64 * WPR * j < nc; ++k) {
+        f32x4_t* at = sums + (k * p.H + 8 * (t + 64 * WPR * j)) / 4;
+        at[0] = at[1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) aw[LDS_SUMS ? 0 : j][i] = an[LDS_SUMS ? 0 : j][i] = 0.0f;
+    }
+  }
   struct Row {
     Raw8<S32> v[CPT], d[CPT];
     Raw8<false> dh[CPT], y[CPT], gt[CPT];
@@ -331,8 +353,9 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             D[j][i] += rn * (e[i] * w[i]) - f[i] * kn;
-            an[j][i] += e[i] * f[i] * rn;
+            e[i] = e[i] * f[i] * rn;
           }
+          add(1, j, e);
         }
         Raw8<S32> o;
         o.set(D[j]);
@@ -364,8 +387,9 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             s2[0] += D[j][i] * w[i] * f[i];
-            aw[j][i] += D[j][i] * f[i] * ry;
+            f[i] = D[j][i] * f[i] * ry;
           }
+          add(0, j, f);
         }
       }
     }
@@ -377,7 +401,7 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
 #pragma unroll
       for (int j = 0; j < CPT; ++j) {
         const int c = t + 64 * WPR * j;
-        if (c < nc) {
+          if (c < nc) {
           float f[8], w[8];
           y[j].get(f);
           load_weight(p.weight, p.weight32, 8 * c, w);
@@ -402,7 +426,7 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
       if (WPR == 1) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) comb[(wave * 8 + i) * 64 + t] = k ? an[j][i] : aw[j][i];
+        for (int i = 0; i < 8; ++i) comb[(wave * 8 + i) * 64 + t] = (k ? an : aw)[LDS_SUMS ? 0 : j][i];
         __syncthreads();
         // wave w adds elements 2 w, 2 w + 1 of every chunk, in wave order
 #pragma unroll
@@ -413,8 +437,15 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
           if (c < nc) part[(int64_t)k * p.H + 8 * c + 2 * wave + i] = s;
         }
       } else if (c < nc) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) part[(int64_t)k * p.H + 8 * c + i] = k ? an[j][i] : aw[j][i];
+        f32x4_t* to = (f32x4_t*)(part + (int64_t)k * p.H + 8 * c);
+        if (LDS_SUMS) {
+          to[0] = sums[(k * p.H + 8 * c) / 4];
+          to[1] = sums[(k * p.H + 8 * c) / 4 + 1];
+        } else {
+          const float(&f)[8] = (k ? an : aw)[LDS_SUMS ? 0 : j];
+          to[0] = f32x4_t{f[0], f[1], f[2], f[3]};
+          to[1] = f32x4_t{f[4], f[5], f[6], f[7]};
+        }
       }
     }
   }
@@ -494,20 +525,24 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_quantize(int64_t rows, int
   }
 }
 
-// Threads of a row: a wave where it holds the row in at most four chunks a
-// lane, else four, eight or sixteen waves.  Few rows take four waves each, to
-// shorten the one row's way.
+// Threads of a row: a wave where it holds the row in at most WAVE_CPT chunks a
+// lane, else four or eight waves.  Few rows take four waves each, to shorten
+// the one row's way.  WAVE_CPT: 4 for the forward norms (8192 x 2048 at 5 TB/s),
+// 2 for the gradients, whose registers hold no more beside the sums, and for
+// the quantiser (8192 x 2048 13.2 us by four waves, 15.7 by one; 4096 x 1024
+// 5.8 and 5.1).
 struct RowPlan {
   int wpr, cpt;
 };
-RowPlan row_plan(int64_t rows, int H, int max_wave_cpt) {
+template <int WAVE_CPT>
+RowPlan row_plan(int64_t rows, int H) {
   const int nc = H / 8;
-  if (rows >= 1024 && nc <= 64 * max_wave_cpt) return {1, nc <= 64 ? 1 : nc <= 128 ? 2 : 4};
+  if (rows >= 1024 && nc <= 64 * WAVE_CPT) return {1, nc <= 64 ? 1 : nc <= 128 ? 2 : 4};
   if (nc <= 64) return {1, 1};
   if (nc <= 256) return {4, 1};
   if (nc <= 512) return {4, 2};
   if (nc <= 1024) return {8, 2};
-  return {16, 2};
+  return {8, 4};
 }
 
 template <int WPR, int CPT, bool MERGE>
@@ -520,22 +555,26 @@ hipError_t fwd(const NormArgs& a, hipStream_t s) {
 template <int WPR, int CPT, bool MERGE>
 hipError_t bwd(const NormArgs& a, unsigned grid, hipStream_t s) {
   const Launch lc{s, nullptr, nullptr};
-  if (a.stream32) return launch(lc, k_norm_bwd<WPR, CPT, true, MERGE>, dim3(grid), dim3(64 * kWaves<WPR>), a);
-  return launch(lc, k_norm_bwd<WPR, CPT, false, MERGE>, dim3(grid), dim3(64 * kWaves<WPR>), a);
+  const size_t shm = WPR == 8 && CPT == 4 ? (size_t)a.H * 8 : 0;  // its sums of the weight gradients
+  if (a.stream32) return launch_shm(lc, k_norm_bwd<WPR, CPT, true, MERGE>, dim3(grid), dim3(64 * kWaves<WPR>), shm, a);
+  return launch_shm(lc, k_norm_bwd<WPR, CPT, false, MERGE>, dim3(grid), dim3(64 * kWaves<WPR>), shm, a);
 }
 
 // calls f(WPR, CPT) with the plan's values as constants
-template <class F>
-hipError_t with_plan(RowPlan r, F&& f) {
+template <int WAVE_CPT, class F>
+hipError_t with_plan(int64_t rows, int H, F&& f) {
+  const RowPlan r = row_plan<WAVE_CPT>(rows, H);
 #define MOE_CASE(W, C) \
   if (r.wpr == W && r.cpt == C) return f(std::integral_constant<int, W>{}, std::integral_constant<int, C>{});
   MOE_CASE(1, 1)
   MOE_CASE(1, 2)
-  MOE_CASE(1, 4)
+  if constexpr (WAVE_CPT == 4) {
+    MOE_CASE(1, 4)
+  }
   MOE_CASE(4, 1)
   MOE_CASE(4, 2)
   MOE_CASE(8, 2)
-  MOE_CASE(16, 2)
+  MOE_CASE(8, 4)
 #undef MOE_CASE
   return hipErrorInvalidValue;
 }
@@ -543,14 +582,14 @@ hipError_t with_plan(RowPlan r, F&& f) {
 }  // namespace
 
 int norm_grad_groups(int64_t rows, int H) {
-  const RowPlan r = row_plan(rows, H, 2);
+  const RowPlan r = row_plan<2>(rows, H);
   const int64_t units = r.wpr == 1 ? (rows + 3) / 4 : rows;
-  const int64_t most = r.wpr == 1 ? 1024 : r.wpr == 4 ? 1024 : r.wpr == 8 ? 512 : 256;
+  const int64_t most = r.wpr < 8 ? 1024 : r.cpt == 2 ? 512 : 256;
   return (int)(units < most ? units : most);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, bool merge, hipStream_t s) {
-  return with_plan(row_plan(a.rows, a.H, 4), [&](auto w, auto c) {
+  return with_plan<4>(a.rows, a.H, [&](auto w, auto c) {
     return merge ? fwd<w(), c(), true>(a, s) : fwd<w(), c(), false>(a, s);
   });
 }
@@ -558,7 +597,7 @@ hipError_t launch_norm_fwd(const NormArgs& a, bool merge, hipStream_t s) {
 hipError_t launch_norm_bwd(const NormArgs& a, bool merge, hipStream_t s) {
   const int groups = norm_grad_groups(a.rows, a.H);
   if (groups > 0) {
-    const hipError_t e = with_plan(row_plan(a.rows, a.H, 2), [&](auto w, auto c) {
+    const hipError_t e = with_plan<2>(a.rows, a.H, [&](auto w, auto c) {
       return merge ? bwd<w(), c(), true>(a, groups, s) : bwd<w(), c(), false>(a, groups, s);
     });
     if (e != hipSuccess) return e;
@@ -570,7 +609,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, bool merge, hipStream_t s) {
 
 hipError_t launch_quantize_i8(int64_t rows, int K, int64_t ldx, const uint16_t* x, int8_t* codes, float* scale,
                               hipStream_t s) {
-  return with_plan(row_plan(rows, K, 2), [&](auto w, auto c) {
+  return with_plan<2>(rows, K, [&](auto w, auto c) {
     constexpr int WPR = w(), CPT = c();
     const unsigned grid = row_grid<WPR>(rows);
     return launch(Launch{s, nullptr, nullptr}, k_quantize<WPR, CPT>, dim3(grid), dim3(64 * kWaves<WPR>), rows, K, ldx,
