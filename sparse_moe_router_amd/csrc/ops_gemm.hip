@@ -514,6 +514,9 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       wait_vm<RB0 + 2 * RB1>();  // all columns, first row half of step 0
       bar();
       read_b(0, 0);
+      // read by every wave before the first memory part refills it
+      wait_vm<63>();
+      bar();
       if (wm == 1) bar();
       for (int s0 = 0; s0 < nsteps; s0 += 2) {
 #pragma unroll
