@@ -69,6 +69,7 @@ struct window_t {
   u32x4_t d;  // buffer descriptor: base, stride 0, range in bytes, raw format
 };
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every range
+// (A scalar offset must stay below the window's range, against whose rest lanes are checked.)
 constexpr int64_t kRange = 0x7FFFFFFF;  // largest range of a descriptor
 __device__ __forceinline__ window_t window(const char* base, int64_t bytes) {
   const uint32_t n = bytes < 0 ? 0u : bytes > kRange ? (uint32_t)kRange : (uint32_t)bytes;
@@ -750,8 +751,11 @@ hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, 
   t.stream = g.K % 64 == 0 && (int64_t)g.E * g.N * g.K * (fp32 ? 4 : 2) > ((int64_t)1 << 28);
   const unsigned grid = (unsigned)op_tile_units(kind, g);
   const Launch lc{s, nullptr, nullptr};
-  // gathered rows past the range of a buffer descriptor are fetched by 64-bit addresses
-  const bool far = g.perm && ((g.x_rows - 1) * g.ldx + g.K) * (i8 ? 1 : 2) > kRange;
+  // Gathered rows past the range of a buffer descriptor are fetched by 64-bit addresses.  So are they
+  // where x has no row at all: every index then stands for zeros, which that form reads from kZero,
+  // while a descriptor of range 0 would not hold lanes back at the later steps' scalar offsets (the
+  // check is against range - scalar offset, which wraps).
+  const bool far = g.perm && (g.x_rows == 0 || ((g.x_rows - 1) * g.ldx + g.K) * (i8 ? 1 : 2) > kRange);
   const dim3 gr(grid), bl(512);
   if (kind == OP_TN) {
     if (!g.perm) return launch(lc, k_op_wgrad<GX_ROWS>, gr, bl, t);
