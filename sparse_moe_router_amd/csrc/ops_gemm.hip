@@ -61,10 +61,9 @@ struct TileArgs {
 // counts them itself, and the compiler, which tells apart at most eight
 // destinations of transfers in flight, would wait for all of them at every LDS
 // read of a ninth.  A wait of the compiler's own for another load counts later
-// transfers as if they were not there and so only waits longer.  m0, the LDS
-// address of a transfer, is otherwise unused on this architecture but for
-// register indexing, which these kernels have none of; the wait states cover a
-// scalar operand that a vector instruction has just written.
+// transfers as if they were not there and so only waits longer.  m0 is the LDS
+// address of a transfer; the wait states cover a scalar operand that a vector
+// instruction has just written.
 struct window_t {
   u32x4_t d;  // buffer descriptor: base, stride 0, range in bytes, raw format
 };
@@ -76,11 +75,15 @@ __device__ __forceinline__ window_t window(const char* base, int64_t bytes) {
   const uint64_t b = (uint64_t)base;
   return window_t{u32x4_t{(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, n, 0x00020000u}};
 }
+// The compiler warns of a clobber of m0, which it allocates to nothing; it does honour it where it
+// keeps a value of m0 of its own.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 // lane i of the wave writes the 16 bytes at offset off + step_off of the window to LDS address dst + 16 i
 __device__ __forceinline__ void dma(window_t w, uint32_t off, int step_off, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst), "v"(off),
                "s"(w.d), "s"(step_off)
-               : "memory");
+               : "memory", "m0");
 }
 // the same with the non-temporal hint: weights that one workgroup alone reads leave the caches to the
 // rows (4096 tokens x 8 over 256 experts 249 -> 226 us; weights that several tiles read lose by it,
@@ -89,14 +92,15 @@ __device__ __forceinline__ void dma(window_t w, uint32_t off, int step_off, uint
 __device__ __forceinline__ void dma_once(window_t w, uint32_t off, int step_off, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(dst), "v"(off),
                "s"(w.d), "s"(step_off)
-               : "memory");
+               : "memory", "m0");
 }
 // by 64-bit addresses, for rows of x that lie more than a descriptor's range apart
 __device__ __align__(16) const uint32_t kZero[4] = {0, 0, 0, 0};
 __device__ __forceinline__ void dma64(const char* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src)
-               : "memory");
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
          (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
