@@ -3,8 +3,10 @@
 //
 //   block_norm    h = x r w,                        r = rsqrt(mean x^2 + eps)
 //   block_merge   out = residual + a s(gate) y r w, then h = out r' w'
-//   gradient of n = v r w for dn:  dv = r (dn w) - v r^3 mean(dn w v),
+//   gradient of n = v r w for dn:  dv = r (dn w - (v r) mean(dn w v r)),
 //                                  dw = sum over rows of dn v r
+//   (in this order: r^3 of a row of zeros and a small eps is past fp32, and
+//   that of a row of 1e15 below it)
 //
 // All are bound by HBM: a row is read once into registers (as it is stored,
 // 16 bytes a lane a load), its sums go through wave shuffles (and LDS when
@@ -326,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
       }
     }
     row_sum<WPR, 3>(s1, lds);
-    const float rn = rsqrtf(s1[0] * rh + p.eps), kn = rn * rn * rn * (s1[1] * rh);
+    const float rn = rsqrtf(s1[0] * rh + p.eps), mn = s1[1] * rh * rn;
     const float ry = rsqrtf(s1[2] * rh + p.eps);
     float gs = p.scale;  // the block output's factor where it is one for the whole row
     float gslope = 0.0f;
@@ -352,8 +354,9 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
           load_weight(wn, p.weight32, 8 * c, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            D[j][i] += rn * (e[i] * w[i]) - f[i] * kn;
-            e[i] = e[i] * f[i] * rn;
+            f[i] *= rn;
+            D[j][i] += rn * (e[i] * w[i] - f[i] * mn);
+            e[i] *= f[i];
           }
           add(1, j, e);
         }
@@ -397,7 +400,7 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
       row_sum<WPR, 2>(s2, lds);
       if (p.gate_mode == MOE_GATE_TOKEN && t == 0)
         ((uint16_t*)p.d_gate.data)[row] = (uint16_t)f32_to_bf16(p.scale * s2[1] * gslope);
-      const float ky = ry * ry * ry * (s2[0] * rh);
+      const float my = s2[0] * rh * ry;
 #pragma unroll
       for (int j = 0; j < CPT; ++j) {
         const int c = t + 64 * WPR * j;
@@ -406,7 +409,7 @@ __global__ __launch_bounds__(64 * kWaves<WPR>) void k_norm_bwd(NormArgs p) {
           y[j].get(f);
           load_weight(p.weight, p.weight32, 8 * c, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = ry * (D[j][i] * w[i]) - f[i] * ky;
+          for (int i = 0; i < 8; ++i) f[i] = ry * (D[j][i] * w[i] - f[i] * ry * my);
           Raw8<false> o;
           o.set(f);
           o.store(p.d_y.data, row * p.d_y.ld + 8 * c);
