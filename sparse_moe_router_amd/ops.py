@@ -217,12 +217,13 @@ def block_merge_grad(d_out: Optional[torch.Tensor], y: torch.Tensor, weight: tor
 def block_forward(x: torch.Tensor, router_w: torch.Tensor, expert_w: torch.Tensor, shared_w: Optional[torch.Tensor],
                   top_k: int, norm_weight: Optional[torch.Tensor], merge_weight: torch.Tensor, eps: float,
                   gate: Optional[torch.Tensor] = None, scale: float = 1.0,
-                  next_weight: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, stream=None, **layer):
+                  next_weight: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, stream=None,
+                  out: Optional[torch.Tensor] = None, **layer):
     """A whole MoE block around :func:`sparse_moe_router_amd.forward`: the norm before it, the layer, and
     the merge after it: ``block_merge(x, forward(h, ...), merge_weight, ...)`` with ``h =
     block_norm(x, norm_weight)``, or the h that the block before gave (norm_weight is then None).
 
-    x is the residual stream (bf16 or fp32 [tokens, H]); gate, scale and next_weight as in
+    x is the residual stream (bf16 or fp32 [tokens, H]); gate, scale, next_weight and out as in
     :func:`block_merge`, whose result is returned; other keywords go to ``forward``."""
     if (h is None) == (norm_weight is None):
         raise ValueError("either norm_weight or h must be given")
@@ -238,4 +239,4 @@ def block_forward(x: torch.Tensor, router_w: torch.Tensor, expert_w: torch.Tenso
             layer["workspace"] = torch.empty(moe.workspace_size(M, H, E, *sizes, top_k, layer.get("flags", 0)),
                                              dtype=torch.uint8, device=h.device)
         y = moe.forward(h, router_w, expert_w, shared_w, top_k, **layer)
-        return block_merge(x, y, merge_weight, eps, gate=gate, scale=scale, next_weight=next_weight)
+        return block_merge(x, y, merge_weight, eps, gate=gate, scale=scale, next_weight=next_weight, out=out)

@@ -1,0 +1,50 @@
+"""block_forward's handling of its arguments: which of its three parts each one reaches."""
+import pytest
+import torch
+
+from ops_util import randn
+from sparse_moe_router_amd import moe, ops
+
+BF16 = torch.bfloat16
+EPS = 1e-6
+
+
+def block(device, M=6, H=128, E=8, I=64):
+    g = torch.Generator().manual_seed(1)
+    w = lambda *s: (torch.randn(*s, generator=g) * 0.05).to(BF16).to(device)
+    return dict(x=randn(2, M, H).to(device), router_w=w(E, H), expert_w=w(E, 3 * I * H), shared_w=None, top_k=2,
+                norm_weight=1 + w(H), merge_weight=1 + w(H), eps=EPS)
+
+
+@pytest.fixture
+def parts(monkeypatch):
+    """The three parts replaced by ones that record their keywords (no GPU)."""
+    seen = {}
+
+    def part(name):
+        def f(x, *a, **kw):
+            seen[name] = kw
+            return x
+        return f
+
+    for mod, name in ((ops, "block_norm"), (moe, "forward"), (ops, "block_merge")):
+        monkeypatch.setattr(mod, name, part(name))
+    return seen
+
+
+def test_out_is_the_blocks_result(parts):
+    b = block("cpu")
+    out = torch.empty_like(b["x"])
+    ops.block_forward(**b, out=out)
+    assert parts["block_merge"]["out"] is out and "out" not in parts["forward"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stream", [BF16, torch.float32])
+def test_out_holds_the_result(stream):
+    b = block("cuda")
+    b["x"] = b["x"].to(stream)
+    want = ops.block_forward(**b)
+    out = torch.full_like(b["x"], 7.0)
+    got = ops.block_forward(**b, out=out)
+    assert got is out and torch.equal(out, want)
