@@ -232,7 +232,7 @@ def block_forward(x: torch.Tensor, router_w: torch.Tensor, expert_w: torch.Tenso
     with torch.cuda.stream(stream):  # and its device
         if h is None:
             h = block_norm(x, norm_weight, eps)
-        if "workspace" not in layer:
+        if layer.get("workspace") is None:
             # of the call's own, as every workspace here: captured graphs never share one
             (M, H), E = h.shape, router_w.shape[0]
             sizes = expert_w.numel() // (3 * E * H), 0 if shared_w is None else shared_w.numel() // (3 * H)

@@ -48,3 +48,18 @@ def test_out_holds_the_result(stream):
     out = torch.full_like(b["x"], 7.0)
     got = ops.block_forward(**b, out=out)
     assert got is out and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("given", [{}, {"workspace": None}])
+def test_workspace_is_the_calls_own(parts, given):
+    """Not the layer's cached one, which captured graphs would share; a caller's is handed on."""
+    b = block("cpu")
+    seen = []
+    for _ in range(2):
+        ops.block_forward(**b, **given)
+        seen.append(parts["forward"]["workspace"])
+    need = moe.workspace_size(6, 128, 8, 64, 0, 2)
+    assert all(w is not None and w.numel() >= need for w in seen) and seen[0] is not seen[1]
+    mine = torch.empty(need, dtype=torch.uint8)
+    ops.block_forward(**b, workspace=mine)
+    assert parts["forward"]["workspace"] is mine
