@@ -232,11 +232,12 @@ def block_forward(x: torch.Tensor, router_w: torch.Tensor, expert_w: torch.Tenso
     with torch.cuda.stream(stream):  # and its device
         if h is None:
             h = block_norm(x, norm_weight, eps)
+        (M, H), E = h.shape, router_w.shape[0]
         if layer.get("workspace") is None:
             # of the call's own, as every workspace here: captured graphs never share one
-            (M, H), E = h.shape, router_w.shape[0]
             sizes = expert_w.numel() // (3 * E * H), 0 if shared_w is None else shared_w.numel() // (3 * H)
             layer["workspace"] = torch.empty(moe.workspace_size(M, H, E, *sizes, top_k, layer.get("flags", 0)),
                                              dtype=torch.uint8, device=h.device)
-        y = moe.forward(h, router_w, expert_w, shared_w, top_k, **layer)
+        # without rows there is nothing to route; torch's empty tensors have no address, which the layer refuses
+        y = moe.forward(h, router_w, expert_w, shared_w, top_k, **layer) if M > 0 else torch.empty_like(h)
         return block_merge(x, y, merge_weight, eps, gate=gate, scale=scale, next_weight=next_weight, out=out)

@@ -63,3 +63,15 @@ def test_workspace_is_the_calls_own(parts, given):
     mine = torch.empty(need, dtype=torch.uint8)
     ops.block_forward(**b, workspace=mine)
     assert parts["forward"]["workspace"] is mine
+
+
+def test_no_rows_skip_the_layer(parts):
+    ops.block_forward(**block("cpu", M=0))
+    assert "forward" not in parts and "block_merge" in parts
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    b = block("cuda", M=0)
+    out, h = ops.block_forward(**b, next_weight=b["norm_weight"])
+    assert out.shape == h.shape == (0, 128)
