@@ -95,13 +95,17 @@ def _fp32(dtype) -> int:
         raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {dtype}") from None
 
 
+def _same_device(stream, *args):
+    for a in args:
+        if isinstance(a, torch.Tensor) and a.is_cuda and a.device != stream.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {a.device}")
+
+
 def _call(stream, f, *args):
     """f on `stream`: that stream and its device are current while it runs."""
     if stream is None:
         return f(*args)
-    for a in args:
-        if isinstance(a, torch.Tensor) and a.is_cuda and a.device != stream.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {a.device}")
+    _same_device(stream, *args)
     with torch.cuda.stream(stream):
         return f(*args)
 
@@ -229,6 +233,8 @@ def block_forward(x: torch.Tensor, router_w: torch.Tensor, expert_w: torch.Tenso
         raise ValueError("either norm_weight or h must be given")
     if stream is None and x.is_cuda:
         stream = torch.cuda.current_stream(x.device)
+    elif stream is not None:
+        _same_device(stream, x, h)
     with torch.cuda.stream(stream):  # and its device
         if h is None:
             h = block_norm(x, norm_weight, eps)

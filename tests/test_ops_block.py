@@ -1,4 +1,6 @@
 """block_forward's handling of its arguments: which of its three parts each one reaches."""
+import types
+
 import pytest
 import torch
 
@@ -75,3 +77,14 @@ def test_no_rows():
     b = block("cuda", M=0)
     out, h = ops.block_forward(**b, next_weight=b["norm_weight"])
     assert out.shape == h.shape == (0, 128)
+
+
+@pytest.mark.gpu
+def test_a_stream_of_another_device_is_refused():
+    """(Its parts would otherwise run on the tensors' own device's current stream and on the other's.)"""
+    b = block("cuda")
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        ops.block_forward(**b, stream=other)
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        ops.block_norm(b["x"], b["norm_weight"], EPS, stream=other)
