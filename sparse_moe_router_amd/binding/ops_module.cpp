@@ -176,9 +176,16 @@ int32_t dim32(int64_t v, const char* name) {
   return (int32_t)v;
 }
 
-// rows of the grouped order: those of out, else of perm, else of x
+// rows of the grouped order: those of perm, else of x.  An out of another number of rows is refused
+// with the permutation's shape, here (fewer than x: its last rows would not be computed) or by the
+// library (more than x).
 int64_t forward_rows(Call& c, PyObject* out, PyObject* perm, const Tensor& x) {
-  if (given(out)) return c.tensor(out, {BF16, F32}, 2, "out").size(0);
+  if (given(out)) {
+    const Tensor& t = c.tensor(out, {BF16, F32}, 2, "out");
+    if (!given(perm) && t.size(0) < x.size(0))
+      value_error("out must have a row for each of x's " + std::to_string(x.size(0)) + ", got " + shape_of(t));
+    return t.size(0);
+  }
   if (given(perm)) return c.tensor(perm, {I32}, 1, "perm").size(0);
   return x.size(0);
 }

@@ -39,3 +39,13 @@ def test_no_rows_of_x(kind):
         ops.grouped_matmul_i8(x, codes(1, E, N, K).cuda(), scales(2, E, N).cuda(), off, perm=perm, top_k=2, out=y,
                               x_scale=None if tokens else torch.empty(0, device="cuda"))
     assert (y == 0).all()
+
+
+def test_out_of_fewer_rows_than_x_is_refused():
+    """A product of x's rows has a row for each of them."""
+    x, w, off = randn(1, 12, 64).cuda(), randn(2, 2, 32, 64).cuda(), offsets_of([5, 7]).cuda()
+    out = torch.empty(11, 32, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="out"):
+        ops.grouped_matmul(x, w, off, out=out)
+    with pytest.raises(ValueError, match="out"):
+        ops.grouped_matmul_i8(x, codes(3, 2, 32, 64).cuda(), scales(4, 2, 32).cuda(), off, out=out)
