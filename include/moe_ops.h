@@ -16,7 +16,8 @@
  * owned by the caller and 16-byte aligned (workspaces 256-byte), nothing
  * allocated, no state between calls, asynchronous on `stream`, arguments
  * checked before anything is enqueued, outputs and workspaces disjoint from
- * every input and from each other.  Work runs on the current device: make the
+ * every input and from each other (element by element where both are column
+ * slices with rows the same number of bytes apart, else as whole extents).  Work runs on the current device: make the
  * stream's device current.  A call with no rows returns MOE_OK without reading
  * its input rows; gradients of weights are then written as zeros.
  */

@@ -591,7 +591,7 @@ moe_status_t moe_tile_weights(int64_t nblocks, int32_t H, int32_t I, const void*
   if (I < 64 || I > 16384 || I % 64) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(src, 16) || !aligned(dst, 16)) return MOE_ERR_MISALIGNED;
   const size_t bytes = (size_t)nblocks * 3 * I * H * 2;
-  if (overlap(src, bytes, dst, bytes)) return MOE_ERR_INVALID_ARG;
+  if (overlap(bytes_at(src, bytes), bytes_at(dst, bytes))) return MOE_ERR_INVALID_ARG;
   if (nblocks == 0) return MOE_OK;
   const hipError_t e = launch_tile_weights((const uint16_t*)src, (uint16_t*)dst, nblocks, H, I, stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);

@@ -17,11 +17,6 @@ constexpr int64_t kMaxLd = 1 << 20;  // 256 rows stay within the range of a buff
 
 constexpr int kInsideElems = 16384;
 
-// bytes from the first to the last element of a [rows][cols] buffer of row stride ld
-size_t extent(int64_t rows, int64_t ld, int64_t cols, int es) {
-  return rows > 0 ? (size_t)((rows - 1) * ld + cols) * es : 0;
-}
-
 struct Checked {
   Groups g;
   size_t w_elems;
@@ -133,20 +128,20 @@ struct NormBuffers {
   Regions r;
   moe_status_t st = MOE_OK;
   enum Kind { STREAM, ACT, GATE };
-  size_t check(const moe_mat_t& m, Kind k) {
-    if (!m.data) return 0;
+  Region check(const moe_mat_t& m, Kind k) {
+    if (!m.data) return bytes_at(nullptr, 0);
     if (!aligned(m.data, 16)) fail(MOE_ERR_MISALIGNED);
-    if (k == GATE && d->gate_mode == MOE_GATE_TOKEN) return (size_t)d->rows * 2;
+    if (k == GATE && d->gate_mode == MOE_GATE_TOKEN) return bytes_at(m.data, (size_t)d->rows * 2);
     if (m.ld < d->H) fail(MOE_ERR_INVALID_ARG);
     if (m.ld > ((int64_t)1 << 31)) fail(MOE_ERR_UNSUPPORTED_SHAPE);
     if (m.ld % 8) fail(MOE_ERR_MISALIGNED);
-    return extent(d->rows, m.ld, d->H, k == STREAM && d->stream_type == MOE_DT_FP32 ? 4 : 2);
+    return matrix_at(m.data, d->rows, m.ld, d->H, k == STREAM && d->stream_type == MOE_DT_FP32 ? 4 : 2);
   }
   void fail(moe_status_t s) {
     if (st == MOE_OK) st = s;
   }
-  void in(const moe_mat_t& m, Kind k) { r.input(m.data, check(m, k)); }
-  void out(const moe_mat_t& m, Kind k) { r.output(m.data, check(m, k)); }
+  void in(const moe_mat_t& m, Kind k) { r.input(check(m, k)); }
+  void out(const moe_mat_t& m, Kind k) { r.output(check(m, k)); }
   void weight(const void* w) {
     if (!aligned(w, 16)) fail(MOE_ERR_MISALIGNED);
     r.input(w, (size_t)d->H * (d->weight_type == MOE_DT_FP32 ? 4 : 2));
@@ -184,10 +179,10 @@ moe_status_t moe_grouped_matmul(const moe_groups_t* d, const void* x, const void
   if (!all_aligned({x, w, y})) return MOE_ERR_MISALIGNED;
   const bool f32 = y_type == MOE_DT_FP32;
   Regions r;
-  r.input(x, extent(d->x_rows, d->ldx, d->K, 2));
+  r.input(matrix_at(x, d->x_rows, d->ldx, d->K, 2));
   r.input(w, c.w_elems * 2);
   group_regions(&r, c.g);
-  r.output(y, extent(d->rows, d->ldy, d->N, f32 ? 4 : 2));
+  r.output(matrix_at(y, d->rows, d->ldy, d->N, f32 ? 4 : 2));
   if (!r.disjoint()) return MOE_ERR_INVALID_ARG;
   return run_forward(false, c.g, x, w, Scales{}, y, f32, stream);
 }
@@ -205,10 +200,10 @@ moe_status_t moe_grouped_matmul_grad_input(const moe_groups_t* d, const void* dy
   const bool f32 = dx_type == MOE_DT_FP32;
   c.g.perm = nullptr;
   Regions r;
-  r.input(dy, extent(d->rows, d->ldy, d->N, 2));
+  r.input(matrix_at(dy, d->rows, d->ldy, d->N, 2));
   r.input(w, c.w_elems * 2);
   group_regions(&r, c.g);
-  r.output(dx, extent(d->rows, d->ldx, d->K, f32 ? 4 : 2));
+  r.output(matrix_at(dx, d->rows, d->ldx, d->K, f32 ? 4 : 2));
   if (!r.disjoint()) return MOE_ERR_INVALID_ARG;
   return run_tile(OP_NN, c.g, dy, w, dx, f32, stream);
 }
@@ -225,8 +220,8 @@ moe_status_t moe_grouped_matmul_grad_weight(const moe_groups_t* d, const void* x
   if (!all_aligned({x, dy, dw})) return MOE_ERR_MISALIGNED;
   const bool f32 = dw_type == MOE_DT_FP32;
   Regions r;
-  r.input(x, extent(d->x_rows, d->ldx, d->K, 2));
-  r.input(dy, extent(d->rows, d->ldy, d->N, 2));
+  r.input(matrix_at(x, d->x_rows, d->ldx, d->K, 2));
+  r.input(matrix_at(dy, d->rows, d->ldy, d->N, 2));
   group_regions(&r, c.g);
   r.output(dw, c.w_elems * (f32 ? 4 : 2));
   if (!r.disjoint()) return MOE_ERR_INVALID_ARG;
@@ -244,7 +239,7 @@ moe_status_t moe_quantize_i8(int64_t rows, int32_t K, int64_t ldx, const void* x
   if (!x || !codes || !scale) return MOE_ERR_INVALID_ARG;
   if (!all_aligned({x, codes, scale})) return MOE_ERR_MISALIGNED;
   Regions r;
-  r.input(x, extent(rows, ldx, K, 2));
+  r.input(matrix_at(x, rows, ldx, K, 2));
   r.output(codes, (size_t)rows * K);
   r.output(scale, (size_t)rows * 4);
   if (!r.disjoint()) return MOE_ERR_INVALID_ARG;
@@ -272,13 +267,13 @@ moe_status_t moe_matmul_i8(const moe_groups_t* d, const void* x, const float* x_
   if (!all_aligned({x, x_scale, w, w_scale, bias, y})) return MOE_ERR_MISALIGNED;
   const bool f32 = y_type == MOE_DT_FP32;
   Regions r;
-  r.input(x, extent(d->x_rows, d->ldx, d->K, x_scale ? 1 : 2));
+  r.input(matrix_at(x, d->x_rows, d->ldx, d->K, x_scale ? 1 : 2));
   r.input(x_scale, (size_t)d->x_rows * 4);
   r.input(w, c.w_elems);
   r.input(w_scale, (size_t)d->E * d->N * 4);
   r.input(bias, (size_t)d->N * 4);
   group_regions(&r, c.g);
-  r.output(y, extent(d->rows, d->ldy, d->N, f32 ? 4 : 2));
+  r.output(matrix_at(y, d->rows, d->ldy, d->N, f32 ? 4 : 2));
   Scales sc{x_scale, w_scale, bias};
   if (!x_scale) {
     const size_t need = moe_matmul_i8_workspace_size(d);
