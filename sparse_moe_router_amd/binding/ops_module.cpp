@@ -9,6 +9,7 @@
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 
 #include <initializer_list>
 #include <string>
@@ -51,6 +52,7 @@ typedef std::initializer_list<at::ScalarType> Types;
 struct Call {
   int device = -1, before = -1;
   hipStream_t stream = nullptr;
+  bool warned = false;
 
   // a tensor argument; the first one fixes the device
   const Tensor& tensor(PyObject* o, Types types, int dims, const char* name) {
@@ -71,6 +73,13 @@ struct Call {
     }
     if (t.dim() != dims)
       value_error(std::string(name) + " must have " + std::to_string(dims) + " dimension(s), got " + shape_of(t));
+    if (t.requires_grad() && c10::GradMode::is_enabled() && !warned) {
+      warned = true;
+      // at the line that calls ops.py
+      const std::string text = std::string(name) + " requires a gradient, which this call does not record: use its "
+                               "gradient call, from torch.no_grad() or a torch.autograd.Function";
+      if (PyErr_WarnEx(PyExc_UserWarning, text.c_str(), 3) != 0) throw PythonError{};
+    }
     return t;
   }
   // a contiguous tensor of exactly this shape; its address

@@ -11,7 +11,8 @@ current stream of its tensors' device, or on ``stream``; what the caller does
 not pass is allocated there, workspaces among it, so that calls on different
 streams and captured graphs never share one; tensors written on other streams
 must be ready on it.  Nothing is recorded for automatic differentiation: the
-gradients are calls of their own.
+gradients are calls of their own, and a tensor that requires a gradient where
+torch records them gives a warning.
 
 ``offsets`` (int32 [E+1]) and ``perm`` (int32 [rows]) are the group offsets and
 the permutation that :func:`sparse_moe_router_amd.route` reports.
