@@ -6,6 +6,7 @@
 
 #include "api_checks.h"
 #include "ops_internal.h"
+#include "ops_paths.h"
 
 using namespace moe;
 
@@ -14,8 +15,6 @@ namespace {
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 constexpr int kMaxN = 1 << 20, kMaxK = 16384;
 constexpr int64_t kMaxLd = 1 << 20;  // 256 rows stay within the range of a buffer descriptor
-
-constexpr int kInsideElems = 16384;
 
 struct Checked {
   Groups g;
@@ -55,28 +54,8 @@ void group_regions(Regions* r, const Groups& g) {
 
 bool check_type(moe_dtype_t t) { return t == MOE_DT_BF16 || t == MOE_DT_FP32; }
 
-// Matrix-vector or matrix-matrix kernel for y = x W^T.  The latter takes the
-// time of one tile's reduction however few tiles there are (measured 5.7 us +
-// 2.9 ns a byte of a weight row); the former 3 us + the touched weights (at most
-// min(E, rows) experts') at 3.9 TB/s, by 1/43 longer for each row of a group.  The
-// first is less while the touched weight rows, so weighted, are fewer than 3.9
-// TB/s * 2.9 ns = about 12000, whatever their length.  Both sides, us
-// (matrix-vector / matrix-matrix): rows of 4 KB, N 4096, one expert: 8 rows 6.5 /
-// 16.2, 64 rows 12.1 / 16.8, 128 rows 22.8 / 21.0; N 1024, top-8 of 256: 1 token
-// 8.9 / 19.0, 2 tokens 18.3 / 19.3, 4 tokens 34.9 / 24.1; N 8192 of 16 KB: 16 rows
-// 38.5 / 53.0, 64 rows 82 / 55; N 2048 of 1 KB, top-8: 1 token 10.8 / 9.6; N 4096 of
-// 128 B: 8 rows 3.9 / 4.3, 64 rows 5.2 / 4.7.
-constexpr int64_t kSkinnyRows = 12000;
-bool skinny(const Groups& g) {
-  const int64_t groups = g.rows < g.E ? g.rows : g.E;
-  return g.N * (43 * groups + g.rows) < 43 * kSkinnyRows;
-}
-
-// bf16 tokens for int8 weights that the matrix-vector kernel quantises itself,
-// every workgroup for its own use, instead of a launch before it (one token, K
-// 2048, N 4096: 4.9 against 6.1 us and 2 us less of host time): up to four
-// tokens and 16384 elements, 64 elements a thread.
-bool quantize_inside(const Groups& g) { return skinny(g) && g.x_rows <= 4 && g.x_rows * g.K <= kInsideElems; }
+bool skinny(const Groups& g) { return takes_matrix_vector(g.rows, g.E, g.N); }
+bool quantize_inside(const Groups& g) { return quantizes_inside(g.rows, g.x_rows, g.E, g.N, g.K); }
 
 // The forward product of either kind on checked arguments.
 moe_status_t run_forward(bool i8, const Groups& g, const void* x, const void* w, const Scales& sc, void* y, bool fp32,

@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "ops_internal.h"
+#include "ops_paths.h"
 #include "quantize8.h"
 
 namespace moe {
@@ -23,7 +24,7 @@ namespace {
 constexpr int SN = 16;  // weight rows of a workgroup
 constexpr int SW = 4;   // waves
 constexpr int SUN = 16;  // 64-byte steps of a wave's run
-constexpr int QR = 4;    // rows quantised at a time by a workgroup
+constexpr int QR = kInsideRows;  // rows quantised at a time by a workgroup
 
 __device__ __align__(16) const uint32_t kZero[4] = {0, 0, 0, 0};
 
