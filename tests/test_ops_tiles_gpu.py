@@ -1,12 +1,14 @@
-"""The matrix-matrix kernels of the products where rows, strides or indexes go wrong: every call here is
-large enough for them (few rows take the matrix-vector kernel)."""
+"""The matrix-matrix kernels of the products where rows, strides or indexes go wrong: calls that are large
+enough for them (few rows take the matrix-vector kernel)."""
 import pytest
 import torch
 
-from ops_util import offsets_of, randn
+import test_ops_grouped_gpu as grouped_tests
+import test_ops_i8_gpu as i8_tests
+from ops_paths import takes_matrix_vector
+from ops_util import F8, close, eps_of, grouped_ref, offsets_of, quantize_ref, randn, source_rows, take
 from sparse_moe_router_amd import ops
 
-pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
 
 
@@ -20,12 +22,101 @@ def scales(seed, *shape):
     return torch.rand(shape, generator=g) * 0.01 + 1e-3
 
 
+def test_both_kernels_have_their_tests():
+    """Which side of the kernel rule the cases of the other files fall on (those of the tests there that
+    come in a small and a large form, among them)."""
+    side = {n: takes_matrix_vector(sum(c), len(c), N) for n, (c, N, K) in grouped_tests.CASES.items()}
+    assert {n for n in side if side[n]} == {"one", "one_expert", "wide_k", "long_k", "decode", "small_batch"}
+    side = {n: takes_matrix_vector(sum(c), len(c), N) for n, (c, N, K) in i8_tests.GROUPED.items()}
+    assert {n for n in side if side[n]} == {"decode"}
+    assert {M for M, N, K in i8_tests.DENSE if not takes_matrix_vector(M, 1, N)} == {257, 600}
+    # rows, experts and outputs of: rows behind the last group, strided rows, entries out of range, offsets out of
+    # order, values that are not finite, rows gathered from far apart, strided and extreme codes, far codes,
+    # graphs and streams (routed, and dense int8)
+    large = [(427, 3, 72), (370, 2, 88), (290, 2, 40), (400, 2, 32), (490, 3, 72), (700, 2, 72), (300, 1, 40),
+             (300, 1, 24), (600, 1, 40), (800, 5, 264), (400, 1, 264)]
+    small = [(44, 3, 72), (9, 3, 88), (8, 2, 40), (8, 2, 32), (12, 3, 72), (12, 2, 72), (5, 1, 40), (8, 8, 80), (4, 1, 80)]
+    assert not any(takes_matrix_vector(*c) for c in large) and all(takes_matrix_vector(*c) for c in small)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", ["bf16", "int8 tokens", "int8 codes"])
+def test_gathered_strided_rows(kind, dtype):
+    """Every tile height, several panels, reductions that end inside a step; x and y column slices beside NaN and
+    a pattern; entries of the permutation that stand for zeros; rows behind the last group; a row of x that is
+    not finite."""
+    counts, N, K, k, extra = [300, 0, 70, 130, 200], 1048, 1040, 2, 9
+    R, E, off = sum(counts), len(counts), offsets_of(counts)
+    assert not takes_matrix_vector(R + extra, E, N)
+    M = 360
+    perm = torch.randperm(M * k, generator=torch.Generator().manual_seed(6))[:R + extra].to(torch.int32)
+    perm[1], perm[301], perm[R - 1], perm[400] = -1, M * k, 2 ** 31 - 1, -2 ** 31
+    bad = int(perm[20]) // k
+    yb = torch.full((R + extra, N + 16), 5.0, dtype=dtype, device="cuda")
+    y = yb[:, 8:8 + N]
+    src = source_rows(R, perm[:R], k, M)
+    tokens = randn(1, M, K)
+    if kind != "int8 codes":
+        tokens[bad, 5] = float("inf")
+        xb = torch.full((M, K + 24), float("nan"), dtype=BF16)
+        xb[:, 8:8 + K] = tokens
+        x = xb.cuda()[:, 8:8 + K]
+    if kind == "bf16":
+        w = randn(2, E, N, K, scale=0.1)
+        ops.grouped_matmul(x, w.cuda(), off.cuda(), perm=perm.cuda(), top_k=k, out=y)
+        want, tol = grouped_ref(take(tokens, src), w, off)
+    else:
+        w, ws = codes(2, E, N, K), scales(3, E, N)
+        q, s = quantize_ref(tokens)
+        xs = None
+        if kind == "int8 codes":
+            s = s.float()
+            s[bad] = float("inf")
+            xs, s = s.cuda(), s.to(F8)
+            q[bad] = 0
+            qb = torch.full((M, K + 48), 99, dtype=torch.int8)
+            qb[:, 16:16 + K] = q.to(torch.int8)
+            x = qb.cuda()[:, 16:16 + K]
+        ops.grouped_matmul_i8(x, w.cuda(), ws.cuda(), off.cuda(), perm=perm.cuda(), top_k=k, x_scale=xs, out=y)
+        qr = take(q, src)
+        sr = torch.where(src >= 0, s[src.clamp(min=0)], torch.zeros((), dtype=F8))
+        want, tol = torch.zeros(R, N, dtype=F8), torch.zeros(R, N, dtype=F8)
+        for e in range(E):
+            a, b = int(off[e]), int(off[e + 1])
+            want[a:b], tol[a:b] = i8_tests.i8_ref(qr[a:b], sr[a:b], w[e], ws[e])
+    rows = (src == bad).nonzero().flatten()
+    got = y[:R].cpu()
+    assert not torch.isfinite(got[rows]).any()
+    keep = torch.ones(R, dtype=torch.bool)
+    keep[rows] = False
+    close(got[keep], want[keep], tol[keep] + eps_of(dtype) * want[keep].abs(), kind)
+    assert (yb[:, :8] == 5).all() and (yb[:, 8 + N:] == 5).all() and (y[R:] == 5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(700, 1048, 1040), (300, 264, 4112), (1030, 72, 144)])
+def test_dense_codes_with_bias(M, N, K, dtype):
+    """The bias in every panel and tile, codes and result in column slices."""
+    assert not takes_matrix_vector(M, 1, N)
+    qb = codes(1, M, K + 16)
+    w, ws, xs, b = codes(2, N, K), scales(3, N), scales(4, M), randn(5, N, dtype=F32)
+    yb = torch.full((M, N + 8), 5.0, dtype=dtype, device="cuda")
+    ops.matmul_i8(qb.cuda()[:, :K], w.cuda(), ws.cuda(), x_scale=xs.cuda(), bias=b.cuda(), out=yb[:, :N])
+    want, tol = i8_tests.i8_ref(qb[:, :K].to(F8), xs.to(F8), w, ws, b)
+    close(yb[:, :N], want, tol + eps_of(dtype) * want.abs())
+    assert (yb[:, N:] == 5).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "int8 tokens", "int8 codes"])
 def test_no_rows_of_x(kind):
     """A permutation that no row of x backs: rows of zeros in every tile height and every step of the
     reduction, and weight gradients of zeros."""
     counts, N, K = [300, 90, 200, 150], 1024, 1040
     R, E, off = sum(counts), len(counts), offsets_of(counts).cuda()
+    assert not takes_matrix_vector(R, E, N)
     perm = torch.arange(R, dtype=torch.int32, device="cuda")
     y = torch.full((R, N), 7.0, device="cuda")
     if kind == "bf16":
@@ -41,6 +132,7 @@ def test_no_rows_of_x(kind):
     assert (y == 0).all()
 
 
+@pytest.mark.gpu
 def test_out_of_fewer_rows_than_x_is_refused():
     """A product of x's rows has a row for each of them."""
     x, w, off = randn(1, 12, 64).cuda(), randn(2, 2, 32, 64).cuda(), offsets_of([5, 7]).cuda()
