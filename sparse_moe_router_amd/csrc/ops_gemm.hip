@@ -49,7 +49,6 @@ struct TileArgs {
   int fp32;
   int npan;    // tiles along the second output dimension
   int nrow;    // TN: tiles along n
-  int stream;  // TN: results are written past the caches
 };
 
 // Transfers go through range-checked buffer descriptors: a lane whose offset
@@ -623,12 +622,6 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       }
     }
   }
-  auto put = [&](auto* at, auto value) {
-    if (KIND == OP_TN && p.stream)
-      __builtin_nontemporal_store(value, at);
-    else
-      *at = value;
-  };
   // 32 x 64 results at a time through a part of the LDS of the wave's own, then 16 bytes a lane
   float* stage = (float*)(lds + HU) + wave * (32 * 64);
   auto write = [&](auto type) {
@@ -665,7 +658,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
           const int row = c / (64 / EC), at = c % (64 / EC) * EC;  // column among the wave's 64
           const int grow = row0 + row, col = c0 + col_of(at >> 5, wn) + (at & 31);
           if (grow < nrows && col < ncols)
-            put((u32x4_t*)((T*)p.out + (row_base + grow) * ldo + col), *(const u32x4_t*)(st + row * 64 + at));
+            *(u32x4_t*)((T*)p.out + (row_base + grow) * ldo + col) = *(const u32x4_t*)(st + row * 64 + at);
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -750,9 +743,6 @@ hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, 
   t.fp32 = fp32;
   t.nrow = (g.N + TB - 1) / TB;
   t.npan = ((kind == OP_NT ? g.N : g.K) + TB - 1) / TB;
-  // weight gradients larger than the last-level cache (256 MB) in whole cache lines: 32768 rows over
-  // 256 experts, 1 GB: 386 -> 355 us
-  t.stream = g.K % 64 == 0 && (int64_t)g.E * g.N * g.K * (fp32 ? 4 : 2) > ((int64_t)1 << 28);
   const unsigned grid = (unsigned)op_tile_units(kind, g);
   const Launch lc{s, nullptr, nullptr};
   // Gathered rows past the range of a buffer descriptor are fetched by 64-bit addresses.  So are they
