@@ -118,7 +118,9 @@ typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_ELEMENT = 2 } moe
  * residual stream (residual, out and their gradients) is bf16 or fp32; h, y,
  * the gate and their gradients are bf16; norm weights are bf16 or fp32 [H],
  * all of one call of the same type; gradients of weights are fp32 [H].
- * Statistics are fp32; each result is rounded once to its type. */
+ * Statistics are fp32, so that a row's sum of squares has to stay below fp32's
+ * largest value (elements up to 1e17 do at every H); each result is rounded once
+ * to its type. */
 typedef struct {
   int64_t rows;            /* tokens, < 2^31 */
   int32_t H;

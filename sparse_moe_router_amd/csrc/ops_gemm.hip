@@ -19,14 +19,15 @@
 // a map made by a launch of its own.
 //
 // Large tiles are bound by the K loop: 16384 rows, 4 experts of 4096 x 4096:
-// 445 us = 1.24 PFLOP/s (NT), 436 us (NN), 416 us = 1.32 (TN); int8 8192^3 2.4 to
+// 451 us = 1.22 PFLOP/s (NT), 448 us (NN), 430 us = 1.28 (TN); int8 8192^3 2.4 to
 // 2.6 POP/s (against 1.38 PFLOP/s and 2.0 POP/s of library products here).  Its
 // clusters alone, without transfers, run at 1.65 (NT) to 2.0 PFLOP/s (TN), the
 // transfers and LDS reads alone at the time of 1.33 to 1.6: what the two cost
 // each other is what is left.  Many small experts are bound by the stream of
-// the weights (32768 rows over 256 experts of 1024 x 2048: 215 us = 5.6 TB/s),
-// and weight gradients over short groups by their results, which nothing
-// overlaps with the next tile's loads (the same rows: 377 us for 1.07 GB).
+// the weights (4096 tokens x 8 over 256 experts of 1024 x 2048: 220 us = 5.3 TB/s
+// of weights, tokens and results, 1158 MB), and weight gradients over short
+// groups by their results, which nothing overlaps with the next tile's loads
+// (the same rows: 395 us for 1.07 GB in bf16, 560 us for 2.15 GB in fp32).
 #include <type_traits>
 
 #include "ops_internal.h"

@@ -7,8 +7,9 @@
 // each in runs of 1 KB of every weight row, straight from global memory into
 // the MFMA operands (16x16 blocks: lane l holds 16 bytes of row l % 16),
 // sixteen weight loads in flight a wave; the four partial sums meet in LDS and
-// are added in wave order.  The weights are read once and, as such, with the
-// non-temporal hint; the few activation rows come from the caches.  Tokens in
+// are added in wave order.  The weights are read once for each 64 rows of a group
+// (once in all for most calls: the host gives it at most 256 rows), and so with
+// the non-temporal hint; the few activation rows come from the caches.  Tokens in
 // bf16 for int8 weights are quantised by every workgroup for itself while its
 // first weights are on their way, when they are few: a launch of its own and
 // its results' way through memory cost more.
