@@ -83,3 +83,14 @@ def test_the_kernel_that_runs(rows, E, N):
     want = {product} if quantizes_inside(rows, rows, E, N, K) else {product, "k_quantize"}
     ops.grouped_matmul_i8(x, wq, ws, off)
     assert kernels(lambda: ops.grouped_matmul_i8(x, wq, ws, off)) == want
+
+
+@pytest.mark.gpu
+def test_rows_without_tokens_quantised_inside():
+    """Rows that no token backs, on the path whose workgroups quantise their rows themselves."""
+    N, K, R, E = 48, 528, 7, 2
+    assert quantizes_inside(R, 0, E, N, K)
+    w = torch.randint(-127, 128, (E, N, K), generator=torch.Generator().manual_seed(3), dtype=torch.int8).cuda()
+    y = ops.grouped_matmul_i8(torch.empty(0, K, dtype=BF16, device="cuda"), w, torch.ones(E, N, device="cuda"),
+                              offsets_of([3, 4]).cuda(), perm=torch.arange(R, dtype=torch.int32, device="cuda"), top_k=2)
+    assert y.shape == (R, N) and (y == 0).all()
