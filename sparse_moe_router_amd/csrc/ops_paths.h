@@ -24,7 +24,8 @@ namespace moe {
 //    weight rows of 512 B, 2 KB and 8 KB: 64 rows 5.3 / 5.6, 7.2 / 10.6 and 20 /
 //    30 us, 128 rows 9.0 / 6.8, 12.8 / 12.8 and 38 / 37, 256 rows 16 / 10, 24 / 20
 //    and 74 / 63, 4096 rows 236 / 10, 476 / 21 and 1276 / 63 (N 8 to 1024 and int8
-//    the same within 10% but for N 392 and more of 8 KB, 39 / 50 at 128 rows).
+//    much the same; by tiles, N 392 and more of 8 KB take 44 us for 64 rows and 50
+//    for 128).
 //    Several groups share their rows, evenly or not: 256 rows of 2 KB over 4
 //    groups of N 64 take 7.4 / 11.7 evenly and 23.8 / 21.5 when one group has
 //    them all, over 16 groups 4.5 / 11.4 and 23.5 / 21.3; 512 rows of one of 4
