@@ -11,6 +11,14 @@
  *   block norms        RMSNorm before a block; RMSNorm after it fused with its
  *                      gate, the residual scale, the residual sum and the next
  *                      block's norm; and their gradients
+ *   gated products     h = silu(x G^T) * (x U^T) grouped by expert in one kernel,
+ *                      and the gradient through it and the projection behind it
+ *   combine            a token's weighted sum over its grouped rows, and its
+ *                      gradients
+ *   clipping           the norm over all gradients of a model, and their scaling
+ *   cross entropy      the loss of tokens against a vocabulary from hidden states
+ *                      and vocabulary weights, without keeping the logits, and
+ *                      its gradients
  *
  * The conventions of moe_layer.h hold for every entry point: device pointers
  * owned by the caller and 16-byte aligned (workspaces 256-byte), nothing
@@ -170,6 +178,133 @@ moe_status_t moe_block_merge_grad(const moe_norm_t* d, moe_mat_t d_out, moe_mat_
 /* Workspace of the two gradient calls (partial sums of the weight gradients);
  * 0 when the arguments are invalid. */
 size_t moe_norm_grad_workspace_size(const moe_norm_t* d);
+
+/* ------------------------------------------------------------ gated products */
+
+/* g[p] = x[row(p)] . G_e^T, u[p] = x[row(p)] . U_e^T, h[p] = silu(g[p]) * u[p],
+ * silu(z) = z / (1 + exp(-z)): the two input projections of a gated
+ * feed-forward block with the activation and the product.  The groups as for
+ * moe_grouped_matmul with N the features of each of the two matrices:
+ *   x        bf16 [x_rows][ldx]
+ *   w        bf16 [E][2 N][K]: G_e, then U_e
+ *   h        bf16 [rows][ldy]
+ *   gate_up  not given, or bf16 [rows][ld] of 2 N columns: g, then u, rounded,
+ *            for the backward pass */
+moe_status_t moe_gated_matmul(const moe_groups_t* g, const void* x, const void* w, void* h, moe_mat_t gate_up,
+                              hipStream_t stream);
+
+/* The gradient through y[p] = h[p] . W_e^T and the gate, in one kernel:
+ *   dh[p] = dy[p] . W_e,  s = 1 / (1 + exp(-g)),
+ *   d_gate_up = (dh u s (1 + g (1 - s)), dh g s),  h = g s u
+ * with g and u as gate_up holds them, and h again for the gradient of W.  dh is
+ * not rounded on the way.  N are the columns of dy, K the features:
+ *   dy         bf16 [rows][ldy]
+ *   w          bf16 [E][N][K]
+ *   gate_up, d_gate_up  bf16 [rows][ld] of 2 K columns
+ *   h          bf16 [rows][ldx]
+ * perm, top_k and x_rows are not used. */
+moe_status_t moe_gated_matmul_grad(const moe_groups_t* g, const void* dy, const void* w, moe_mat_t gate_up,
+                                   moe_mat_t d_gate_up, void* h, hipStream_t stream);
+
+/* ------------------------------------------------------------ combine */
+
+/* inverse[a] = the row p with perm[p] == a, the lowest of several, for the
+ * assignments 0 <= a < n; -1 where no row has it.  Rows from the end of the last
+ * group on (offsets[E], when offsets are given; E is else not used) and entries of
+ * perm outside [0, n) count for nothing.  perm int32 [rows], inverse int32 [n];
+ * rows, n < 2^31, E 1 .. 1024. */
+moe_status_t moe_invert_permutation(int64_t rows, const int32_t* perm, const int32_t* offsets, int32_t E, int64_t n,
+                                    int32_t* inverse, hipStream_t stream);
+
+/* Tokens and the grouped rows of their assignments.  H a multiple of 8, 8 <= H <=
+ * 16384; top_k 1 .. 32; tokens * top_k < 2^31. */
+typedef struct {
+  int64_t tokens;
+  int64_t rows;           /* grouped rows */
+  int32_t H;
+  int32_t top_k;
+  int32_t E;              /* with offsets: 1 .. 1024 */
+  moe_dtype_t out_type;   /* of out and add */
+  const int32_t* inverse; /* [tokens * top_k]: as moe_invert_permutation gives it; entries outside [0, rows) have no row */
+  const int32_t* perm;    /* [rows]; gradient only */
+  const int32_t* offsets; /* [E+1] or NULL: all rows; gradient only */
+} moe_combine_t;
+
+/* out[t] = add[t] + sum_s weight[t][s] y[inverse[t * top_k + s]], in the order of
+ * s in fp32, rounded once; an assignment without a row adds nothing, whatever its
+ * weight.  y bf16 [rows][ld], weight fp32 [tokens][top_k] or NULL (ones), add
+ * [tokens][ld] in out's type or not given, out bf16 or fp32 [tokens][ld]. */
+moe_status_t moe_combine(const moe_combine_t* d, moe_mat_t y, const float* weight, moe_mat_t add, moe_mat_t out,
+                         hipStream_t stream);
+
+/* Its gradients: dy[p] = weight[t][s] d_out[t] for the row p of assignment (t, s),
+ * zeros for a row in front of offsets[E] that no assignment has, rows behind it
+ * left as they were; d_weight[t][s] = <d_out[t], y[p]>, 0 for an assignment without
+ * a row.  d_out and y bf16, dy bf16 [rows][ld], d_weight fp32 [tokens][top_k].
+ * Without weight, y is not read and d_weight is NULL; with it d_weight may be
+ * NULL. */
+moe_status_t moe_combine_grad(const moe_combine_t* d, moe_mat_t d_out, moe_mat_t y, const float* weight, moe_mat_t dy,
+                              float* d_weight, hipStream_t stream);
+
+/* ------------------------------------------------------------ clipping */
+
+/* One of many gradients: n elements in a row, aligned as their type only. */
+typedef struct {
+  const void* in;
+  void* out;              /* moe_clip_grads only; in place: out == in of the same type */
+  int64_t n;              /* >= 0; the addresses of a tensor without elements are not used */
+  moe_dtype_t in_type;
+  moe_dtype_t out_type;
+} moe_tensor_t;
+
+/* *norm = sqrt(sum over all elements of all tensors of in^2), fp32.  The sum is of
+ * 64 bits and repeats bit for bit; an infinity or NaN among the elements gives one.
+ * The addresses are read from `tensors` (host memory) during the call.  workspace:
+ * moe_grad_norm_workspace_size bytes (0 when the arguments are invalid). */
+size_t moe_grad_norm_workspace_size(const moe_tensor_t* tensors, int32_t count);
+moe_status_t moe_grad_norm(const moe_tensor_t* tensors, int32_t count, float* norm, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/* out = in * min(1, max_norm / (norm + eps)), rounded once; in place nothing is
+ * written where that factor is 1.  norm_given = 0: *norm is computed and written
+ * first, as above; else it is read (of gradients that other devices hold too, say)
+ * and the workspace is not used.  max_norm >= 0, eps > 0, both finite.  An infinite norm scales
+ * to 0, a NaN to NaN. */
+moe_status_t moe_clip_grads(const moe_tensor_t* tensors, int32_t count, float max_norm, float eps, float* norm,
+                            int32_t norm_given, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------ cross entropy */
+
+/* Tokens against a vocabulary: 1 <= V <= 2^20, H a multiple of 8, 8 <= H <= 16384,
+ * ldx a multiple of 8, H <= ldx <= 2^20, rows < 2^31, and fewer than 2^22 tiles of
+ * 256 x 256 in a matrix of as many rows and of V, or of H, columns.  A token whose target is ignore_index or lies outside
+ * [0, V) has no target: its loss is 0 and it has no part in the gradients. */
+typedef struct {
+  int64_t rows;           /* tokens */
+  int64_t ldx;            /* elements from a row of x to the next */
+  int32_t V;
+  int32_t H;
+  int64_t ignore_index;
+} moe_loss_t;
+
+/* z = x[t] . w^T in fp32, lse[t] = log(sum_v exp(z[v])), loss[t] = lse[t] -
+ * z[target[t]].  x bf16 [rows][ldx], w bf16 [V][H], target int64 [rows], loss and
+ * lse fp32 [rows] (lse may be NULL).  workspace:
+ * moe_cross_entropy_workspace_size bytes. */
+size_t moe_cross_entropy_workspace_size(const moe_loss_t* d);
+moe_status_t moe_cross_entropy(const moe_loss_t* d, const void* x, const void* w, const int64_t* target, float* loss,
+                               float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* dz[t][v] = d_loss[t] (exp(z[t][v] - lse[t]) - (v == target[t])), rounded to bf16;
+ * dx[t] = sum_v dz[t][v] w[v], dw[v] = sum_t dz[t][v] x[t].  lse as the forward call
+ * gave it, d_loss fp32 [rows]; dx bf16 or fp32 [rows][ld] or not given, dw bf16 or
+ * fp32 [V][H] or NULL.  The vocabulary goes by in pieces; the workspace
+ * (moe_cross_entropy_grad_workspace_size bytes) holds one piece's dz and the sums of
+ * dx. */
+size_t moe_cross_entropy_grad_workspace_size(const moe_loss_t* d);
+moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, const void* x, const void* w,
+                                    const int64_t* target, const float* lse, moe_mat_t dx, moe_dtype_t dx_type, void* dw,
+                                    moe_dtype_t dw_type, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

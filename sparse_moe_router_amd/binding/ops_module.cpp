@@ -13,6 +13,7 @@
 
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "moe_ops.h"
 
@@ -500,6 +501,350 @@ PyObject* block_merge_grad(PyObject*, Args a, Py_ssize_t n) {
   });
 }
 
+// x, w, offsets, perm, top_k, save, out, gate_up
+PyObject* gated_matmul(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    Call c;
+    const Tensor& x = c.tensor(a[0], {BF16}, 2, "x");
+    const Tensor& w = c.tensor(a[1], {BF16}, 3, "w");
+    if (w.size(1) % 2) value_error("w must have the rows of two matrices, got " + shape_of(w));
+    moe_groups_t g{};
+    g.E = dim32(w.size(0), "w"), g.N = dim32(w.size(1) / 2, "w"), g.K = dim32(w.size(2), "w");
+    void* wp = c.flat(a[1], {BF16}, {g.E, 2 * (int64_t)g.N, g.K}, "w");
+    const moe_mat_t xm = c.rows(a[0], {BF16}, -1, g.K, "x");
+    g.rows = forward_rows(c, a[6], a[3], x);
+    g.x_rows = x.size(0);
+    set_groups(c, &g, a[2], a[3], a[4]);
+    const int save = PyObject_IsTrue(a[5]);
+    if (save < 0) throw PythonError{};
+    if (given(a[7]) && !save) value_error("gate_up is written with save only");
+    c.begin();
+    Tensor own, pre;
+    if (!given(a[6])) own = c.empty({g.rows, g.N}, BF16);
+    const moe_mat_t hm = given(a[6]) ? c.rows(a[6], {BF16}, -1, g.N, "out") : moe_mat_t{own.data_ptr(), g.N};
+    moe_mat_t pm{nullptr, 0};
+    const int64_t cols = 2 * (int64_t)g.N;
+    if (save)
+      pm = given(a[7]) ? c.rows(a[7], {BF16}, g.rows, cols, "gate_up")
+                       : moe_mat_t{(pre = c.empty({g.rows, cols}, BF16)).data_ptr(), cols};
+    g.ldx = xm.ld, g.ldy = hm.ld;
+    check(moe_gated_matmul(&g, xm.data, wp, hm.data, pm, c.stream), "moe_gated_matmul");
+    PyObject* h = result(a[6], own);
+    if (!save) return h;
+    PyObject* q = result(a[7], pre);
+    PyObject* r = PyTuple_Pack(2, h, q);
+    Py_XDECREF(h);
+    Py_XDECREF(q);
+    return r;
+  });
+}
+
+// dy, w, gate_up, offsets
+PyObject* gated_matmul_grad(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject* {
+    Call c;
+    const Tensor& dy = c.tensor(a[0], {BF16}, 2, "dy");
+    const Tensor& w = c.tensor(a[1], {BF16}, 3, "w");
+    moe_groups_t g{};
+    g.E = dim32(w.size(0), "w"), g.N = dim32(w.size(1), "w"), g.K = dim32(w.size(2), "w");
+    void* wp = c.flat(a[1], {BF16}, {g.E, g.N, g.K}, "w");
+    const moe_mat_t dym = c.rows(a[0], {BF16}, -1, g.N, "dy");
+    g.rows = g.x_rows = dy.size(0);
+    g.top_k = 1;
+    const int64_t cols = 2 * (int64_t)g.K;
+    const moe_mat_t pm = c.rows(a[2], {BF16}, g.rows, cols, "gate_up");
+    if (given(a[3]))
+      g.offsets = (const int32_t*)c.flat(a[3], {I32}, {(int64_t)g.E + 1}, "offsets");
+    else if (g.E != 1)
+      value_error("offsets may be left out with one expert only");
+    c.begin();
+    Tensor d = c.empty({g.rows, cols}, BF16), h = c.empty({g.rows, g.K}, BF16);
+    g.ldx = g.K, g.ldy = dym.ld;
+    check(moe_gated_matmul_grad(&g, dym.data, wp, pm, moe_mat_t{d.data_ptr(), cols}, h.data_ptr(), c.stream),
+          "moe_gated_matmul_grad");
+    return Py_BuildValue("{sNsN}", "gate_up", wrap(d), "h", wrap(h));
+  });
+}
+
+// group offsets of any number of experts; their number
+const int32_t* any_offsets(Call& c, PyObject* o, int32_t* E) {
+  if (!given(o)) return nullptr;
+  const Tensor& t = c.tensor(o, {I32}, 1, "offsets");
+  if (t.size(0) < 2) value_error("offsets must have at least two entries");
+  *E = dim32(t.size(0) - 1, "offsets");
+  return (const int32_t*)c.flat(o, {I32}, {t.size(0)}, "offsets");
+}
+
+// perm, assignments (None: as many as perm), offsets, out
+PyObject* invert_permutation(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject* {
+    Call c;
+    const int64_t rows = c.tensor(a[0], {I32}, 1, "perm").size(0);
+    const void* perm = c.flat(a[0], {I32}, {rows}, "perm");
+    int64_t num = rows;
+    if (given(a[1])) {
+      num = PyLong_AsLongLong(a[1]);
+      if (num == -1 && PyErr_Occurred()) throw PythonError{};
+      if (num < 0) value_error("assignments must not be negative");
+    }
+    int32_t E = 0;
+    const int32_t* offsets = any_offsets(c, a[2], &E);
+    c.begin();
+    Tensor own;
+    void* out = given(a[3]) ? c.flat(a[3], {I32}, {num}, "out") : (own = c.empty({num}, I32)).data_ptr();
+    check(moe_invert_permutation(rows, (const int32_t*)perm, offsets, E, num, (int32_t*)out, c.stream),
+          "moe_invert_permutation");
+    return result(a[3], own);
+  });
+}
+
+// tokens of a combine: inverse holds top_k assignments of each
+void set_combine(Call& c, moe_combine_t* d, const Tensor& inverse, PyObject* top_k) {
+  d->top_k = integer(top_k);
+  if (d->top_k < 1 || inverse.size(0) % d->top_k) value_error("inverse must hold top_k entries for each token");
+  d->tokens = inverse.size(0) / d->top_k;
+}
+
+// y, inverse, top_k, weight, add, out, fp32
+PyObject* combine(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject* {
+    Call c;
+    const Tensor& y = c.tensor(a[0], {BF16}, 2, "y");
+    moe_combine_t d{};
+    const Tensor& inv = c.tensor(a[1], {I32}, 1, "inverse");
+    set_combine(c, &d, inv, a[2]);
+    d.inverse = (const int32_t*)c.flat(a[1], {I32}, {inv.size(0)}, "inverse");
+    d.rows = y.size(0), d.H = dim32(y.size(1), "y");
+    const moe_mat_t ym = c.rows(a[0], {BF16}, d.rows, d.H, "y");
+    const float* w = given(a[3]) ? (const float*)c.flat(a[3], {F32}, {d.tokens, d.top_k}, "weight") : nullptr;
+    const auto type = given(a[5]) ? c.tensor(a[5], {BF16, F32}, 2, "out").scalar_type() : out_type(a[6]);
+    const moe_mat_t am = opt_rows(c, a[4], type, d.tokens, d.H, "add");
+    d.out_type = type == F32 ? MOE_DT_FP32 : MOE_DT_BF16;
+    c.begin();
+    Tensor own;
+    const moe_mat_t om = given(a[5]) ? c.rows(a[5], {type}, d.tokens, d.H, "out")
+                                     : moe_mat_t{(own = c.empty({d.tokens, d.H}, type)).data_ptr(), d.H};
+    check(moe_combine(&d, ym, w, am, om, c.stream), "moe_combine");
+    return result(a[5], own);
+  });
+}
+
+// d_out, y, perm, inverse, weight, top_k, offsets, dy
+PyObject* combine_grad(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    Call c;
+    const Tensor& dout = c.tensor(a[0], {BF16}, 2, "d_out");
+    moe_combine_t d{};
+    d.H = dim32(dout.size(1), "d_out");
+    const moe_mat_t dm = c.rows(a[0], {BF16}, -1, d.H, "d_out");
+    d.rows = c.tensor(a[2], {I32}, 1, "perm").size(0);
+    d.perm = (const int32_t*)c.flat(a[2], {I32}, {d.rows}, "perm");
+    const Tensor& inv = c.tensor(a[3], {I32}, 1, "inverse");
+    d.inverse = (const int32_t*)c.flat(a[3], {I32}, {inv.size(0)}, "inverse");
+    const float* w = nullptr;
+    moe_mat_t ym{nullptr, 0};
+    if (given(a[4])) {
+      const Tensor& wt = c.tensor(a[4], {F32}, 2, "weight");
+      d.top_k = dim32(wt.size(1), "weight");
+      if (given(a[5]) && integer(a[5]) != d.top_k) value_error("weight must have top_k columns, got " + shape_of(wt));
+      d.tokens = dout.size(0);
+      w = (const float*)c.flat(a[4], {F32}, {d.tokens, d.top_k}, "weight");
+      if (!given(a[1])) value_error("y must be given with weight");
+      ym = c.rows(a[1], {BF16}, d.rows, d.H, "y");
+    } else {
+      if (!given(a[5])) value_error("top_k must be given without weight");
+      set_combine(c, &d, inv, a[5]);
+    }
+    if (dout.size(0) != d.tokens || inv.size(0) != d.tokens * d.top_k)
+      value_error("d_out must have a row, and inverse top_k entries, for each token, got " + shape_of(dout) + " and " +
+                  shape_of(inv));
+    d.offsets = any_offsets(c, a[6], &d.E);
+    c.begin();
+    Tensor own, dw;
+    const moe_mat_t dym = given(a[7]) ? c.rows(a[7], {BF16}, d.rows, d.H, "dy")
+                                      : moe_mat_t{(own = c.empty({d.rows, d.H}, BF16)).data_ptr(), d.H};
+    if (w) dw = c.empty({d.tokens, d.top_k}, F32);
+    check(moe_combine_grad(&d, dm, ym, w, dym, w ? (float*)dw.data_ptr() : nullptr, c.stream), "moe_combine_grad");
+    PyObject* res = Py_BuildValue("{sN}", "y", result(a[7], own));
+    if (res && w) {
+      PyObject* v = wrap(dw);
+      if (!v || PyDict_SetItemString(res, "weight", v) != 0) {
+        Py_XDECREF(v);
+        Py_DECREF(res);
+        throw PythonError{};
+      }
+      Py_DECREF(v);
+    }
+    return res;
+  });
+}
+
+// One of many gradients: any shape, contiguous.
+const Tensor& gradient(Call& c, PyObject* o, const char* name, Py_ssize_t i) {
+  if (!THPVariable_Check(o)) type_error(std::string(name) + " must hold torch tensors");
+  const Tensor& t = THPVariable_Unpack(o);
+  auto fail = [&](const std::string& s) { value_error(std::string(name) + "[" + std::to_string(i) + "] " + s); };
+  if (!t.is_cuda()) fail("must be on the GPU, got " + t.device().str());
+  const int d = t.get_device();
+  if (c.device < 0)
+    c.device = d;
+  else if (d != c.device)
+    fail("is on " + t.device().str() + ", the call on cuda:" + std::to_string(c.device));
+  if (t.scalar_type() != BF16 && t.scalar_type() != F32)
+    type_error(std::string(name) + "[" + std::to_string(i) + "] must be BFloat16 or Float, got " +
+               c10::toString(t.scalar_type()));
+  if (!t.is_contiguous()) fail("must be contiguous");
+  return t;
+}
+// The list's tensors; with outs (None: in place) as their results.
+std::vector<moe_tensor_t> gradients(Call& c, PyObject* list, PyObject* outs, bool scaled) {
+  if (!PyList_Check(list) && !PyTuple_Check(list)) type_error("grads must be a list or tuple of tensors");
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
+  if (n == 0) value_error("grads must hold at least one tensor");
+  const bool apart = scaled && given(outs);
+  if (apart) {
+    if (!PyList_Check(outs) && !PyTuple_Check(outs)) type_error("out must be a list or tuple of tensors");
+    if (PySequence_Fast_GET_SIZE(outs) != n) value_error("out must hold a tensor for each gradient");
+  }
+  std::vector<moe_tensor_t> v((size_t)n);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const Tensor& t = gradient(c, PySequence_Fast_GET_ITEM(list, i), "grads", i);
+    moe_tensor_t& m = v[(size_t)i];
+    m.in = t.data_ptr();
+    m.n = t.numel();
+    m.in_type = m.out_type = dt(t);
+    m.out = (void*)m.in;
+    if (!apart) continue;
+    const Tensor& o = gradient(c, PySequence_Fast_GET_ITEM(outs, i), "out", i);
+    if (o.sizes() != t.sizes())
+      value_error("out[" + std::to_string(i) + "] must have shape " + shape_of(t) + ", got " + shape_of(o));
+    m.out = o.data_ptr();
+    m.out_type = dt(o);
+  }
+  return v;
+}
+int32_t count_of(const std::vector<moe_tensor_t>& v) { return dim32((int64_t)v.size(), "grads"); }
+
+// grads, workspace
+PyObject* grad_norm(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 2, [&]() -> PyObject* {
+    Call c;
+    const auto v = gradients(c, a[0], Py_None, false);
+    c.begin();
+    Tensor norm = c.empty({}, F32), wk;
+    size_t have = 0;
+    void* wkp = workspace(c, a[1], moe_grad_norm_workspace_size(v.data(), count_of(v)), &wk, &have);
+    check(moe_grad_norm(v.data(), count_of(v), (float*)norm.data_ptr(), wkp, have, c.stream), "moe_grad_norm");
+    return wrap(norm);
+  });
+}
+
+// grads, max_norm, norm, eps, out, workspace
+PyObject* clip_grads(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    Call c;
+    const auto v = gradients(c, a[0], a[4], true);
+    const double max_norm = number(a[1]), eps = number(a[3]);
+    float* np = nullptr;
+    if (given(a[2])) {
+      const Tensor& t = THPVariable_Check(a[2]) ? c.tensor(a[2], {F32}, (int)THPVariable_Unpack(a[2]).dim(), "norm")
+                                                : c.tensor(a[2], {F32}, 0, "norm");
+      if (t.numel() != 1) value_error("norm must have one element, got " + shape_of(t));
+      np = (float*)t.data_ptr();
+    }
+    c.begin();
+    Tensor norm, wk;
+    void* wkp = nullptr;
+    size_t have = 0;
+    if (!np) {
+      norm = c.empty({}, F32);
+      wkp = workspace(c, a[5], moe_grad_norm_workspace_size(v.data(), count_of(v)), &wk, &have);
+    }
+    check(moe_clip_grads(v.data(), count_of(v), (float)max_norm, (float)eps, np ? np : (float*)norm.data_ptr(), np != nullptr,
+                         wkp, have, c.stream),
+          "moe_clip_grads");
+    return result(a[2], norm);
+  });
+}
+
+// x, w, targets, ignore_index into a descriptor
+struct Loss {
+  moe_loss_t d{};
+  moe_mat_t x;
+  const void* w;
+  const int64_t* target;
+  Loss(Call& c, PyObject* xo, PyObject* wo, PyObject* to, PyObject* ignore) {
+    const Tensor& xt = c.tensor(xo, {BF16}, 2, "x");
+    const Tensor& wt = c.tensor(wo, {BF16}, 2, "w");
+    d.rows = xt.size(0), d.H = dim32(xt.size(1), "x"), d.V = dim32(wt.size(0), "w");
+    x = c.rows(xo, {BF16}, d.rows, d.H, "x");
+    w = c.flat(wo, {BF16}, {d.V, d.H}, "w");
+    target = (const int64_t*)c.flat(to, {at::kLong}, {d.rows}, "targets");
+    d.ldx = x.ld;
+    d.ignore_index = PyLong_AsLongLong(ignore);
+    if (d.ignore_index == -1 && PyErr_Occurred()) throw PythonError{};
+  }
+};
+
+// x, w, targets, ignore_index, workspace
+PyObject* cross_entropy(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    Call c;
+    const Loss l(c, a[0], a[1], a[2], a[3]);
+    c.begin();
+    Tensor loss = c.empty({l.d.rows}, F32), lse = c.empty({l.d.rows}, F32), wk;
+    size_t have = 0;
+    void* wkp = workspace(c, a[4], moe_cross_entropy_workspace_size(&l.d), &wk, &have);
+    check(moe_cross_entropy(&l.d, l.x.data, l.w, l.target, (float*)loss.data_ptr(), (float*)lse.data_ptr(), wkp, have,
+                            c.stream),
+          "moe_cross_entropy");
+    PyObject* r0 = wrap(loss);
+    PyObject* r1 = wrap(lse);
+    PyObject* r = PyTuple_Pack(2, r0, r1);
+    Py_XDECREF(r0);
+    Py_XDECREF(r1);
+    return r;
+  });
+}
+
+// d_loss, x, w, targets, lse, ignore_index, dx fp32 (None: no dx), dw fp32 (None: no dw), workspace
+PyObject* cross_entropy_grad(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    Call c;
+    const Loss l(c, a[1], a[2], a[3], a[5]);
+    const float* dl = (const float*)c.flat(a[0], {F32}, {l.d.rows}, "d_loss");
+    const float* lse = (const float*)c.flat(a[4], {F32}, {l.d.rows}, "lse");
+    c.begin();
+    Tensor dx, dw, wk;
+    moe_mat_t dxm{nullptr, 0};
+    if (given(a[6])) {
+      dx = c.empty({l.d.rows, l.d.H}, out_type(a[6]));
+      dxm = moe_mat_t{dx.data_ptr(), l.d.H};
+    }
+    if (given(a[7])) dw = c.empty({l.d.V, l.d.H}, out_type(a[7]));
+    size_t have = 0;
+    void* wkp = workspace(c, a[8], moe_cross_entropy_grad_workspace_size(&l.d), &wk, &have);
+    check(moe_cross_entropy_grad(&l.d, dl, l.x.data, l.w, l.target, lse, dxm, given(a[6]) ? dt(dx) : MOE_DT_BF16,
+                                 given(a[7]) ? dw.data_ptr() : nullptr, given(a[7]) ? dt(dw) : MOE_DT_BF16, wkp, have,
+                                 c.stream),
+          "moe_cross_entropy_grad");
+    PyObject* res = PyDict_New();
+    auto put = [&](const char* key, Tensor& t) {
+      PyObject* v = wrap(t);
+      if (!v || PyDict_SetItemString(res, key, v) != 0) {
+        Py_XDECREF(v);
+        Py_DECREF(res);
+        throw PythonError{};
+      }
+      Py_DECREF(v);
+    };
+    if (!res) return nullptr;
+    if (given(a[6])) put("x", dx);
+    if (given(a[7])) put("w", dw);
+    return res;
+  });
+}
+
 #define FAST(name) \
   { #name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {FAST(grouped_matmul),
@@ -511,6 +856,15 @@ PyMethodDef methods[] = {FAST(grouped_matmul),
                          FAST(block_norm_grad),
                          FAST(block_merge),
                          FAST(block_merge_grad),
+                         FAST(gated_matmul),
+                         FAST(gated_matmul_grad),
+                         FAST(invert_permutation),
+                         FAST(combine),
+                         FAST(combine_grad),
+                         FAST(grad_norm),
+                         FAST(clip_grads),
+                         FAST(cross_entropy),
+                         FAST(cross_entropy_grad),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -71,6 +71,16 @@ hipError_t launch_quantize_i8(int64_t rows, int K, int64_t ldx, const uint16_t* 
 // Output tiles of a launch; 0 rows give 0.
 int64_t op_tile_units(OpKind kind, const Groups& g);
 
+// Gated products, g.N features of each of the two matrices: h (rows g.ldy apart) from x, and with
+// pre the products themselves; by matrix-matrix tiles or for few rows.
+hipError_t launch_gated(const Groups& g, const void* x, const void* w, void* h, void* pre, int64_t ldp, hipStream_t s);
+hipError_t launch_gated_skinny(const Groups& g, const void* x, const void* w, void* h, void* pre, int64_t ldp,
+                               hipStream_t s);
+int64_t gated_units(const Groups& g);
+// dy W through the gate: d_pre and h of g.K features.
+hipError_t launch_gated_grad(const Groups& g, const void* dy, const void* w, const void* pre, int64_t ldp, void* d_pre,
+                             int64_t ldd, void* h, int64_t ldh, hipStream_t s);
+
 // Block norms: the arguments as the kernels take them (d_* only in the gradients).
 struct NormArgs {
   int64_t rows;
@@ -88,5 +98,70 @@ hipError_t launch_norm_fwd(const NormArgs& a, bool merge, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, bool merge, hipStream_t s);
 // Workgroups of the gradient kernel = partial sums of each weight gradient.
 int norm_grad_groups(int64_t rows, int H);
+
+// A token's sum over its grouped rows, and its gradients (d_* and dy only there).
+struct CombineArgs {
+  int64_t tokens, rows;
+  int H, k, E;
+  const int32_t *perm, *inverse, *offsets;
+  const float* weight;  // [tokens][k] or NULL: ones
+  moe_mat_t y, add, out;
+  moe_mat_t d_out, dy;
+  float* d_weight;
+};
+hipError_t launch_invert(const int32_t* perm, const int32_t* offsets, int E, int64_t rows, int32_t* inverse, int64_t n,
+                         hipStream_t s);
+hipError_t launch_combine(const CombineArgs& a, bool fp32, hipStream_t s);
+hipError_t launch_combine_grad(const CombineArgs& a, hipStream_t s);
+
+// Tensors of one launch over many gradients, cut into pieces; as kernel arguments (below 4 KB).
+constexpr int kClipTensors = 120;
+constexpr int kClipGroups = 2048;  // workgroups of a launch at most
+struct GradTable {
+  const void* in[kClipTensors];
+  void* out[kClipTensors];
+  int64_t n[kClipTensors];
+  int32_t first[kClipTensors];  // first piece
+  uint32_t types[2][4];         // bit j: tensor j of in (0) or out (1) is fp32
+  int32_t count;
+  int32_t pieces;
+  __host__ __device__ bool type(int j, int of_out) const { return types[of_out][j >> 5] >> (j & 31) & 1; }
+};
+static_assert(sizeof(GradTable) < 3840, "kernel arguments");
+int64_t clip_pieces(int64_t n);
+int clip_groups(int64_t pieces);
+hipError_t launch_squares(const GradTable& t, double* part, hipStream_t s);
+hipError_t launch_norm(const double* part, int parts, float* norm, hipStream_t s);
+// part NULL: *norm is given; else it is the root of the parts' sum, and stored if store.
+hipError_t launch_clip(const GradTable& t, const double* part, int parts, float* norm, float max_norm, float eps,
+                       bool store, hipStream_t s);
+
+// Softmax cross entropy against a vocabulary (lse, d_loss, dx and dw only in the gradient).
+struct LossArgs {
+  int64_t rows, ldx;
+  int V, H;
+  const void *x, *w;
+  const int64_t* target;
+  int64_t ignore;
+  float *loss, *lse_out;
+  const float *lse, *d_loss;
+  void* dx;  // or NULL
+  int64_t lddx;
+  bool dx32, dw32;
+  void* dw;  // or NULL
+};
+// The gradient goes through the vocabulary in pieces whose d (bf16) takes at most kLossPieceBytes,
+// but at least kLossPieceColumns columns; dx is summed in `slices` buffers, each over `slice` columns
+// of a piece.
+constexpr int64_t kLossPieceBytes = 64 << 20;
+constexpr int kLossPieceColumns = 2048;
+struct LossPlan {
+  int piece, slice, slices;
+  size_t d_bytes, bytes;
+};
+LossPlan loss_plan(int64_t rows, int V, int H);
+size_t loss_workspace(int64_t rows, int V);
+hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s);
+hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s);
 
 }  // namespace moe

@@ -12,7 +12,8 @@
 // the non-temporal hint; the few activation rows come from the caches.  Tokens in
 // bf16 for int8 weights are quantised by every workgroup for itself while its
 // first weights are on their way, when they are few: a launch of its own and
-// its results' way through memory cost more.
+// its results' way through memory cost more.  Gated products take eight rows of
+// each of the expert's two matrices, whose sums then meet in the same place.
 #include <type_traits>
 
 #include "ops_internal.h"
@@ -36,6 +37,8 @@ struct SkinnyArgs {
   Scales sc;
   void* y;
   int fp32;
+  uint16_t* pre;  // gated: the products themselves (NULL: not kept)
+  int64_t ldp;
   int by_row;  // workgroup row = row of the grouped order (else the expert)
 };
 
@@ -83,8 +86,9 @@ __device__ __forceinline__ void quantize_rows(const SkinnyArgs& p, int64_t p0, i
   __syncthreads();
 }
 
-// QX: x is bf16 and quantised here (rows <= QR, NB = 1).
-template <bool I8, int NB, bool QX>
+// QX: x is bf16 and quantised here (rows <= QR, NB = 1).  GATED: n0 counts the
+// rows of each matrix; the block's rows 0..7 are of the first, 8..15 of the second.
+template <bool I8, int NB, bool QX, bool GATED>
 __device__ __forceinline__ void skinny_block(const SkinnyArgs& p, int e, int n0, int64_t p0, int rows, float* red,
                                              int8_t* codes, float* qscale) {
   typedef typename std::conditional<I8, i32x4_t, f32x4_t>::type acc_t;
@@ -94,8 +98,9 @@ __device__ __forceinline__ void skinny_block(const SkinnyArgs& p, int e, int n0,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KC = g.K * ES / 16;        // 16-byte chunks of a row
   const int steps = (KC + 3) / 4;      // 64-byte steps
-  const int n = n0 + l16;
-  const char* wrow = p.w + ((int64_t)e * g.N + (n < g.N ? n : 0)) * g.K * ES + quad * 16;
+  const int n = GATED ? n0 + (l16 & 7) : n0 + l16;
+  const int64_t first = GATED ? ((int64_t)2 * e + (l16 >> 3)) * g.N : (int64_t)e * g.N;
+  const char* wrow = p.w + (first + (n < g.N ? n : 0)) * g.K * ES + quad * 16;
   const int wlim = n < g.N ? KC : 0;
   u32x4_t wf[SUN];
   auto load_w = [&](int s0) {
@@ -158,6 +163,27 @@ __device__ __forceinline__ void skinny_block(const SkinnyArgs& p, int e, int n0,
 #pragma unroll
   for (int b = 0; b < NB; ++b) *(acc_t*)(rd + ((wave * 16 * NB) + 16 * b + l16) * 16 + 4 * quad) = acc[b];
   __syncthreads();
+  if constexpr (GATED) {
+    for (int i = threadIdx.x; i < rows * 4; i += 64 * SW) {  // two features a thread
+      const int r = i >> 2, c = 2 * (i & 3);
+      float v[2][2] = {};
+#pragma unroll
+      for (int w = 0; w < SW; ++w)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          v[m][0] += rd[(w * 16 * NB + r) * 16 + 8 * m + c];
+          v[m][1] += rd[(w * 16 * NB + r) * 16 + 8 * m + c + 1];
+        }
+      *(uint32_t*)((uint16_t*)p.y + (p0 + r) * g.ldy + n0 + c) =
+          pack_bf16x2(silu(v[0][0]) * v[1][0], silu(v[0][1]) * v[1][1]);
+      if (p.pre) {
+        uint16_t* o = p.pre + (p0 + r) * p.ldp + n0 + c;
+        *(uint32_t*)o = pack_bf16x2(v[0][0], v[0][1]);
+        *(uint32_t*)(o + g.N) = pack_bf16x2(v[1][0], v[1][1]);
+      }
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < rows * 8; i += 64 * SW) {  // two weight rows a thread
     const int r = i >> 3, c = 2 * (i & 7), col = n0 + c;
     if (col >= g.N) continue;
@@ -185,13 +211,13 @@ __device__ __forceinline__ void skinny_block(const SkinnyArgs& p, int e, int n0,
   }
 }
 
-template <bool I8, bool QX>
+template <bool I8, bool QX, bool GATED = false>
 __global__ __launch_bounds__(64 * SW) void k_op_skinny(SkinnyArgs p) {
   __shared__ float red[QX ? SW * 16 * 16 : SW * 64 * 16];
   __shared__ float qscale[QR];
   extern __shared__ u32x4_t codes[];  // QX: QR rows of K + 16 bytes
   const Groups& g = p.g;
-  const int n0 = blockIdx.x * SN;
+  const int n0 = blockIdx.x * (GATED ? SN / 2 : SN);
   int e = blockIdx.y;
   if (p.by_row) {
     // the expert of row blockIdx.y, taken by the workgroup of its first row
@@ -211,17 +237,31 @@ __global__ __launch_bounds__(64 * SW) void k_op_skinny(SkinnyArgs p) {
     constexpr int MAXR = QX ? QR : 64;
     const int rows = (int)(hi - lo < MAXR ? hi - lo : MAXR);
     if (QX || rows <= 16)
-      skinny_block<I8, 1, QX>(p, e, n0, lo, rows, red, (int8_t*)codes, qscale);
+      skinny_block<I8, 1, QX, GATED>(p, e, n0, lo, rows, red, (int8_t*)codes, qscale);
     else if (rows <= 32)
-      skinny_block<I8, 2, false>(p, e, n0, lo, rows, red, nullptr, nullptr);
+      skinny_block<I8, 2, false, GATED>(p, e, n0, lo, rows, red, nullptr, nullptr);
     else
-      skinny_block<I8, 4, false>(p, e, n0, lo, rows, red, nullptr, nullptr);
+      skinny_block<I8, 4, false, GATED>(p, e, n0, lo, rows, red, nullptr, nullptr);
     lo += rows;
     if (lo < hi) __syncthreads();  // the partial sums are read before they are overwritten
   }
 }
 
 }  // namespace
+
+hipError_t launch_gated_skinny(const Groups& g, const void* x, const void* w, void* h, void* pre, int64_t ldp,
+                               hipStream_t s) {
+  SkinnyArgs a{};
+  a.g = g;
+  a.x = (const char*)x;
+  a.w = (const char*)w;
+  a.y = h;
+  a.pre = (uint16_t*)pre;
+  a.ldp = ldp;
+  a.by_row = g.offsets && g.rows < g.E;
+  const dim3 grid((unsigned)((g.N + SN / 2 - 1) / (SN / 2)), (unsigned)(a.by_row ? g.rows : g.E));
+  return launch(Launch{s, nullptr, nullptr}, k_op_skinny<false, false, true>, grid, dim3(64 * SW), a);
+}
 
 hipError_t launch_op_skinny(bool i8, bool quantize, const Groups& g, const void* x, const void* w, const Scales& sc, void* y,
                             bool fp32, hipStream_t s) {

@@ -1,5 +1,7 @@
 """The operators in ``include/moe_ops.h`` on torch tensors: products grouped by
-expert with their gradients, 8-bit products, and the norms around a block.
+expert with their gradients, 8-bit products, the norms around a block, and what a
+training step needs beside them: gated products, the sum over a token's experts,
+clipping and the loss.
 
 Argument marshalling only, as in :mod:`.moe`: torch tensors provide device
 memory and the stream, every step runs in the library's HIP kernels, and a
@@ -34,8 +36,10 @@ except ImportError as e:  # not built, or built against another torch
 
 EXPORTS = ("moe_grouped_matmul", "moe_grouped_matmul_grad_input", "moe_grouped_matmul_grad_weight",
            "moe_quantize_i8", "moe_matmul_i8_workspace_size", "moe_matmul_i8", "moe_block_norm",
-           "moe_block_norm_grad", "moe_block_merge", "moe_block_merge_grad", "moe_norm_grad_workspace_size")
-
+           "moe_block_norm_grad", "moe_block_merge", "moe_block_merge_grad", "moe_norm_grad_workspace_size",
+           "moe_gated_matmul", "moe_gated_matmul_grad", "moe_invert_permutation", "moe_combine", "moe_combine_grad",
+           "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_clip_grads", "moe_cross_entropy_workspace_size",
+           "moe_cross_entropy", "moe_cross_entropy_grad_workspace_size", "moe_cross_entropy_grad")
 
 
 class MoeGroups(ctypes.Structure):
@@ -54,6 +58,22 @@ class MoeMat(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
 
 
+class MoeCombine(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("H", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("out_type", ctypes.c_int), ("inverse", ctypes.c_void_p),
+                ("perm", ctypes.c_void_p), ("offsets", ctypes.c_void_p)]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("in_type", ctypes.c_int),
+                ("out_type", ctypes.c_int)]
+
+
+class MoeLoss(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("V", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("ignore_index", ctypes.c_int64)]
+
+
 
 _bound = None
 
@@ -64,7 +84,8 @@ def lib() -> ctypes.CDLL:
     if _bound is None:
         L = moe.lib()
         vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
-        g, n, en = ctypes.POINTER(MoeGroups), ctypes.POINTER(MoeNorm), ctypes.c_int
+        g, n, en, f32 = ctypes.POINTER(MoeGroups), ctypes.POINTER(MoeNorm), ctypes.c_int, ctypes.c_float
+        c, t, l = ctypes.POINTER(MoeCombine), ctypes.POINTER(MoeTensor), ctypes.POINTER(MoeLoss)
         sig = {
             "moe_grouped_matmul": (en, [g, vp, vp, vp, en, vp]),
             "moe_grouped_matmul_grad_input": (en, [g, vp, vp, vp, en, vp]),
@@ -78,6 +99,18 @@ def lib() -> ctypes.CDLL:
             "moe_block_merge_grad": (en, [n, MoeMat, MoeMat, MoeMat, vp, MoeMat, MoeMat, vp, MoeMat, MoeMat, MoeMat,
                                           vp, vp, vp, sz, vp]),
             "moe_norm_grad_workspace_size": (sz, [n]),
+            "moe_gated_matmul": (en, [g, vp, vp, vp, MoeMat, vp]),
+            "moe_gated_matmul_grad": (en, [g, vp, vp, MoeMat, MoeMat, vp, vp]),
+            "moe_invert_permutation": (en, [i64, vp, vp, i32, i64, vp, vp]),
+            "moe_combine": (en, [c, MoeMat, vp, MoeMat, MoeMat, vp]),
+            "moe_combine_grad": (en, [c, MoeMat, MoeMat, vp, MoeMat, vp, vp]),
+            "moe_grad_norm_workspace_size": (sz, [t, i32]),
+            "moe_grad_norm": (en, [t, i32, vp, vp, sz, vp]),
+            "moe_clip_grads": (en, [t, i32, f32, f32, vp, i32, vp, sz, vp]),
+            "moe_cross_entropy_workspace_size": (sz, [l]),
+            "moe_cross_entropy": (en, [l, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "moe_cross_entropy_grad_workspace_size": (sz, [l]),
+            "moe_cross_entropy_grad": (en, [l, vp, vp, vp, vp, vp, MoeMat, en, vp, en, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -248,3 +281,127 @@ def block_forward(x: torch.Tensor, router_w: torch.Tensor, expert_w: torch.Tenso
         # without rows there is nothing to route; torch's empty tensors have no address, which the layer refuses
         y = moe.forward(h, router_w, expert_w, shared_w, top_k, **layer) if M > 0 else torch.empty_like(h)
         return block_merge(x, y, merge_weight, eps, gate=gate, scale=scale, next_weight=next_weight, out=out)
+
+
+# ------------------------------------------------------------------ gated feed-forward blocks
+
+def gated_matmul(x: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor],
+                 perm: Optional[torch.Tensor] = None, top_k: int = 1, save: bool = False,
+                 out: Optional[torch.Tensor] = None, gate_up: Optional[torch.Tensor] = None, stream=None):
+    """moe_gated_matmul: ``out[p] = silu(x[row(p)] @ w[e, :I].T) * (x[row(p)] @ w[e, I:].T)``, both
+    projections, the activation and the product in one kernel.
+
+    w bf16 [E, 2 I, K] (the gate's rows, then the up projection's); x, offsets, perm and rows as in
+    :func:`grouped_matmul`.  Returns bf16 [rows, I]; with save (out, gate_up), gate_up bf16
+    [rows, 2 I] the two products for :func:`gated_matmul_grad`."""
+    return _call(stream, _ops.gated_matmul, x, w, offsets, perm, top_k, save, out, gate_up)
+
+
+def gated_matmul_grad(dy: torch.Tensor, w: torch.Tensor, gate_up: torch.Tensor, offsets: Optional[torch.Tensor],
+                      stream=None) -> dict:
+    """moe_gated_matmul_grad: the gradient dy of the projection behind a gated product, ``y = h @ w[e].T``
+    with w bf16 [E, H, I], through that projection, the product and the activation, as a dict:
+    ``gate_up`` (bf16 [rows, 2 I]) and ``h`` (bf16 [rows, I], which the gradient of w needs)."""
+    return _call(stream, _ops.gated_matmul_grad, dy, w, gate_up, offsets)
+
+
+def feed_forward(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, offsets: Optional[torch.Tensor],
+                 perm: Optional[torch.Tensor] = None, top_k: int = 1, save: bool = False,
+                 out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16, stream=None):
+    """A gated feed-forward block of every expert: :func:`gated_matmul` with w_gate_up [E, 2 I, K], then
+    :func:`grouped_matmul` with w_down [E, H, I].  Returns y [rows, H]; with save (y, gate_up)."""
+    h = gated_matmul(x, w_gate_up, offsets, perm, top_k, save, stream=stream)
+    h, gate_up = h if save else (h, None)
+    y = grouped_matmul(h, w_down, offsets, out=out, out_dtype=out_dtype, stream=stream)
+    return (y, gate_up) if save else y
+
+
+def feed_forward_grad(dy: torch.Tensor, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                      gate_up: torch.Tensor, offsets: Optional[torch.Tensor], perm: Optional[torch.Tensor] = None,
+                      top_k: int = 1, dw_dtype: torch.dtype = torch.float32, stream=None) -> dict:
+    """The gradients of :func:`feed_forward` from dy (bf16 [rows, H]) and the gate_up that it saved, as a
+    dict: ``x`` (bf16, of each grouped row: :func:`combine` with top_k sums a token's), ``w_gate_up``
+    and ``w_down`` (in dw_dtype; zeros for an expert without rows).  The gradient of gate_up and h are
+    rounded to bf16 between the kernels."""
+    g = gated_matmul_grad(dy, w_down, gate_up, offsets, stream)
+    return dict(x=grouped_matmul_grad_input(g["gate_up"], w_gate_up, offsets, stream=stream),
+                w_gate_up=grouped_matmul_grad_weight(x, g["gate_up"], offsets, perm, top_k, out_dtype=dw_dtype,
+                                                     stream=stream),
+                w_down=grouped_matmul_grad_weight(g["h"], dy, offsets, out_dtype=dw_dtype, stream=stream))
+
+
+# ------------------------------------------------------------------ combine
+
+def invert_permutation(perm: torch.Tensor, assignments: Optional[int] = None, offsets: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_invert_permutation: int32 [assignments] (as many as perm has rows, if not given) with
+    ``inverse[perm[p]] = p``, -1 where no row has the assignment; rows from ``offsets[-1]`` on do not count."""
+    return _call(stream, _ops.invert_permutation, perm, assignments, offsets, out)
+
+
+def combine(y: torch.Tensor, inverse: torch.Tensor, top_k: int, weight: Optional[torch.Tensor] = None,
+            add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """moe_combine: ``out[t] = add[t] + sum_s weight[t, s] * y[inverse[t * top_k + s]]``: a token's output
+    from its experts' rows, and without weight a token's gradient from its copies'.
+
+    y bf16 [rows, H]; inverse as :func:`invert_permutation` gives it; weight fp32 [tokens, top_k]; add
+    and out bf16 or fp32 [tokens, H]."""
+    return _call(stream, _ops.combine, y, inverse, top_k, weight, add, out, _fp32(out_dtype))
+
+
+def combine_grad(d_out: torch.Tensor, y: Optional[torch.Tensor], perm: torch.Tensor, inverse: torch.Tensor,
+                 weight: Optional[torch.Tensor] = None, top_k: Optional[int] = None,
+                 offsets: Optional[torch.Tensor] = None, dy: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """moe_combine_grad: the gradients of :func:`combine` as a dict: ``y`` (bf16 [rows, H], into dy if
+    given) and, with weight, ``weight`` (fp32 [tokens, top_k]).  d_out is also the gradient of add.
+
+    Rows from ``offsets[-1]`` on (with offsets) keep what dy held.  y is needed with weight, top_k
+    without."""
+    return _call(stream, _ops.combine_grad, d_out, y, perm, inverse, weight, top_k, offsets, dy)
+
+
+# ------------------------------------------------------------------ clipping
+
+def grad_norm(grads, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_grad_norm: the 2-norm of all elements of a list of gradients (bf16 or fp32, contiguous, any
+    shapes), an fp32 tensor of no dimensions."""
+    return _call_list(stream, grads, None, _ops.grad_norm, grads, workspace)
+
+
+def clip_grads(grads, max_norm: float, norm: Optional[torch.Tensor] = None, eps: float = 1e-6, out=None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_clip_grads: every gradient times ``min(1, max_norm / (norm + eps))``, in place or into the list
+    out (of the same shapes, bf16 or fp32).  Returns the norm: that of grads, computed by the call, or
+    the given one (fp32, one element on the GPU), which holds the share of other devices, say."""
+    return _call_list(stream, grads, out, _ops.clip_grads, grads, max_norm, norm, eps, out, workspace)
+
+
+def _call_list(stream, grads, out, f, *args):
+    if stream is not None:
+        _same_device(stream, *(grads if isinstance(grads, (list, tuple)) else ()),
+                     *(out if isinstance(out, (list, tuple)) else ()))
+    return _call(stream, f, *args)
+
+
+# ------------------------------------------------------------------ cross entropy
+
+def cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """moe_cross_entropy: (loss, lse), fp32 [tokens] each, of the logits ``x @ w.T`` against targets (int64
+    [tokens]), without keeping the logits: ``lse = logsumexp(logits)``, ``loss = lse - logits[target]``.
+
+    x bf16 [tokens, H], w bf16 [V, H].  A token whose target is ignore_index or lies outside the
+    vocabulary has loss 0 and no gradient."""
+    return _call(stream, _ops.cross_entropy, x, w, targets, ignore_index, workspace)
+
+
+def cross_entropy_grad(d_loss: torch.Tensor, x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                       lse: torch.Tensor, ignore_index: int = -100, dx_dtype: Optional[torch.dtype] = torch.bfloat16,
+                       dw_dtype: Optional[torch.dtype] = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                       stream=None) -> dict:
+    """moe_cross_entropy_grad: the gradients of the loss of :func:`cross_entropy` as a dict ``x`` and ``w``
+    (each in its dtype, left out where that is None), from d_loss (fp32 [tokens]) and the lse that the
+    forward call gave.  The gradient of a logit is rounded to bf16 before the products."""
+    return _call(stream, _ops.cross_entropy_grad, d_loss, x, w, targets, lse, ignore_index,
+                 None if dx_dtype is None else _fp32(dx_dtype), None if dw_dtype is None else _fp32(dw_dtype), workspace)

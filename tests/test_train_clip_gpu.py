@@ -1,0 +1,159 @@
+"""The norm over many gradients and their scaling, against 64 bits: types, sizes around every piece and chunk,
+addresses off 16 bytes, values whose squares fp32 does not hold, many tensors."""
+import math
+
+import pytest
+import torch
+
+from ops_util import EPS32, F8, close, eps_of, randn
+from sparse_moe_router_amd import ops
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+SIZES = [1, 2, 3, 7, 8, 9, 255, 1024, 4097, 32767, 32768, 32769, 65536 + 5, 300001]
+
+
+def norm_of(grads):
+    return math.sqrt(math.fsum(float((t.to(F8) ** 2).sum()) for t in grads))
+
+
+def check_norm(got, grads):
+    # one rounding to fp32 of a sum of doubles (2^-53 a term)
+    want = norm_of(grads)
+    n = sum(t.numel() for t in grads)
+    assert got.dtype == F32 and got.dim() == 0
+    assert abs(got.item() - want) <= (1.001 * EPS32 + n * 2.0 ** -53) * want, (got.item(), want)
+
+
+def scaled(grads, norm, max_norm, eps=1e-6):
+    """Results in 64 bits, and the relative error of a result but for its own rounding: the norm's, the
+    factor's and the product's."""
+    c = min(1.0, max_norm / (norm + eps)) if math.isfinite(norm) else max_norm / (norm + eps)
+    return [t.to(F8) * c for t in grads], 3.01 * EPS32
+
+
+def make(sizes, types, seed=0):
+    return [randn(seed + i, n, scale=10.0 ** (i % 4 - 2), dtype=types[i % len(types)]) for i, n in enumerate(sizes)]
+
+
+@pytest.mark.parametrize("types", [[BF16], [F32], [BF16, F32]], ids=["bf16", "fp32", "mixed"])
+def test_norm_and_scaling(types):
+    grads = make(SIZES, types)
+    dev = [t.cuda() for t in grads]
+    check_norm(ops.grad_norm(dev), grads)
+    for t in dev:
+        check_norm(ops.grad_norm([t]), [t.cpu()])
+    for max_norm in (1.0, 0.0, 1e9):
+        mine = [t.clone() for t in dev]
+        norm = ops.clip_grads(mine, max_norm)
+        check_norm(norm, grads)
+        want, rel = scaled(grads, norm_of(grads), max_norm)
+        for a, b, t in zip(mine, want, grads):
+            close(a, b, (rel + eps_of(t.dtype)) * b.abs())
+        if max_norm == 1e9:
+            assert all(torch.equal(a, b) for a, b in zip(mine, dev)), "nothing to scale"
+
+
+@pytest.mark.parametrize("src", [BF16, F32])
+@pytest.mark.parametrize("dst", [BF16, F32])
+@pytest.mark.parametrize("max_norm", [1.0, 1e9])
+def test_into_other_tensors(src, dst, max_norm):
+    grads = make(SIZES, [src])
+    dev = [t.cuda() for t in grads]
+    out = [torch.full((t.numel(),), 5.0, dtype=dst, device="cuda") for t in grads]
+    norm = ops.clip_grads(dev, max_norm, out=out)
+    want, rel = scaled(grads, norm_of(grads), max_norm)
+    for a, b, t, d in zip(out, want, grads, dev):
+        close(a, b, (rel + eps_of(dst)) * b.abs())
+        assert torch.equal(d.cpu(), t)
+
+
+@pytest.mark.parametrize("src", [BF16, F32])
+@pytest.mark.parametrize("dst", [BF16, F32])
+def test_any_element_of_a_buffer(src, dst):
+    """Slices that start at any element, in and out apart; what lies around them stays."""
+    n = 40000
+    buf = randn(1, n + 64, dtype=src).cuda()
+    for a in range(0, 9):
+        for b in (a, 0, 3):
+            g = buf[a:a + n - a]
+            wide = torch.full((n + 64,), 5.0, dtype=dst, device="cuda")
+            o = wide[b:b + n - a]
+            norm = ops.clip_grads([g], 2.0, out=[o])
+            check_norm(norm, [g.cpu()])
+            (want,), rel = scaled([g.cpu()], norm_of([g.cpu()]), 2.0)
+            close(o, want, (rel + eps_of(dst)) * want.abs())
+            assert (wide[:b] == 5).all() and (wide[b + n - a:] == 5).all()
+
+
+def test_many_tensors_of_one_buffer():
+    """More tensors than a launch takes, side by side in one buffer, as a bucket holds them."""
+    sizes = [1 + (i * 37) % 2000 for i in range(700)]
+    flat = randn(1, sum(sizes), dtype=F32).cuda()
+    grads = list(flat.split(sizes))
+    whole = flat.clone()
+    norm = ops.clip_grads(grads, 3.0)
+    check_norm(norm, [whole.cpu()])
+    (want,), rel = scaled([whole.cpu()], norm_of([whole.cpu()]), 3.0)
+    close(flat, want, (rel + EPS32) * want.abs())
+    assert torch.equal(ops.grad_norm(list(whole.split(sizes))), norm)
+
+
+def test_values_past_fp32_squares():
+    big, small = torch.full((5000,), 1e30), torch.full((5000,), 1e-30)
+    for t in (big, small, torch.cat([big, small])):
+        check_norm(ops.grad_norm([t.cuda()]), [t])
+    t = big.cuda()
+    norm = ops.clip_grads([t], 1.0)
+    close(t, torch.full((5000,), 1.0 / norm_of([big]), dtype=F8) * big.to(F8), 5 * EPS32 * torch.ones(5000, dtype=F8))
+    t = torch.full((1 << 20,), 3e38).cuda()
+    assert torch.isinf(ops.grad_norm([t]))  # the norm itself past fp32
+
+
+def test_infinities_and_nan():
+    t = randn(1, 100, dtype=F32)
+    t[5] = float("inf")
+    a, b = t.cuda(), randn(2, 50).cuda()
+    assert torch.isinf(ops.clip_grads([a, b], 1.0))
+    assert not b.any() and torch.isnan(a[5]) and not a[:5].any()  # times 0
+    t[5] = float("nan")
+    a, b = t.cuda(), randn(2, 50).cuda()
+    assert torch.isnan(ops.clip_grads([a, b], 1.0)) and torch.isnan(b).all() and torch.isnan(a).all()
+
+
+def test_given_norm():
+    g = make([100, 5000], [BF16, F32])
+    for shape in ((), (1,)):
+        dev = [t.cuda() for t in g]
+        n = torch.full(shape, 10.0, device="cuda")
+        assert ops.clip_grads(dev, 2.5, norm=n) is n and n.item() == 10.0
+        want, rel = scaled(g, 10.0, 2.5)
+        for a, b, t in zip(dev, want, g):
+            close(a, b, (rel + eps_of(t.dtype)) * b.abs())
+
+
+def test_empty_and_shaped():
+    e = torch.empty(0, 5, device="cuda")
+    assert ops.grad_norm([e]).item() == 0 and ops.clip_grads([e, e], 1.0).item() == 0
+    t = randn(1, 3, 5, 7, dtype=F32).cuda()
+    check_norm(ops.grad_norm([e, t, torch.ones((), device="cuda")]), [t.cpu(), torch.ones(())])
+
+
+def test_refuses():
+    t = torch.ones(64, 64, device="cuda")
+    for call in (lambda: ops.grad_norm([t.t()[:3]]), lambda: ops.grad_norm([t[:, :3]]), lambda: ops.grad_norm([t, t.cpu()]),
+                 lambda: ops.clip_grads([t], 1.0, out=[t, t]), lambda: ops.clip_grads([t], 1.0, out=[t.view(-1)]),
+                 lambda: ops.clip_grads([t], 1.0, norm=torch.ones(2, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: ops.grad_norm([t.half()]), lambda: ops.grad_norm([t, 1.0]), lambda: ops.clip_grads([t], "a"),
+                 lambda: ops.clip_grads([t], 1.0, out=t), lambda: ops.clip_grads([t], 1.0, norm=1.0)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: ops.clip_grads([t, t], 1.0), lambda: ops.clip_grads([t, t[3:]], 1.0),
+                 lambda: ops.clip_grads([t], -1.0), lambda: ops.clip_grads([t], 1.0, eps=0.0),
+                 lambda: ops.clip_grads([t], 1.0, norm=t[0, :1])):
+        with pytest.raises(ops.MoeError):
+            call()
+    assert (t == 1).all()
+    ops.grad_norm([t, t])  # reading twice is no overlap

@@ -1,0 +1,121 @@
+"""Plain 64-bit forms of the operators of a training step and the tolerances their tests use (the
+conventions of ops_util: EPS32 and EPS16 are half a unit in the last place).
+
+exp, 1 / x: the hardware's exponential of a product with log2(e) is off by at most (2 |z| + 4) EPS32 of
+its value (the product's rounding grows with |z|), a reciprocal by 2 EPS32; RZ(z) below counts both and
+the few roundings of the products around them.  Both give 0 for results below 2^-126, the smallest normal
+number: a sigmoid s(z) of z < -87.3 is then off by up to FLUSH = 2^-126 beside its relative error, and what
+it is multiplied with carries that on: |z| FLUSH for z s(z), (1 + |z|) FLUSH for the slope s (1 + z (1 - s)).
+"""
+import torch
+
+from ops_util import EPS16, EPS32, F8, grouped_ref
+
+
+FLUSH = 2.0 ** -126
+
+
+def rz(z):
+    return (4 * z.abs() + 24) * EPS32
+
+
+def silu(z):
+    return z * torch.sigmoid(z)
+
+
+def gated_ref(rows64, w, offsets):
+    """((h, tol), (gate_up, tol)), tolerances with the roundings of the results."""
+    I = w.shape[1] // 2
+    pre, t = grouped_ref(rows64, w, offsets)
+    g, u, tg, tu = pre[:, :I], pre[:, I:], t[:, :I], t[:, I:]
+    h = silu(g) * u
+    # |silu'| <= 1.1
+    th = 1.1 * tg * u.abs() + silu(g).abs() * tu + 1.1 * tg * tu + h.abs() * rz(g) + (g * u).abs() * FLUSH
+    return (h, th + EPS16 * (h.abs() + th)), (pre, t + EPS16 * (pre.abs() + t))
+
+
+def gated_grad_ref(dy, w, gate_up, offsets):
+    """((d_gate_up, tol), (h, tol)); rows of no group NaN."""
+    dh, t = grouped_ref(dy.to(F8), w.transpose(1, 2), offsets)
+    I = dh.shape[1]
+    g, u = gate_up[:, :I].to(F8), gate_up[:, I:].to(F8)
+    s, n = torch.sigmoid(g), torch.sigmoid(-g)
+    slope, mag = s * (1 + g * n), s * (1 + g.abs() * n)
+    dg, du, h = dh * u * slope, dh * g * s, g * s * u
+    td = torch.cat([t * (u * slope).abs() + (dh.abs() + t) * u.abs() * mag * rz(g),
+                    t * (g * s).abs() + (dh.abs() + t) * (g * s).abs() * rz(g)], 1)
+    far = (dh.abs() + t) * FLUSH
+    td = td + torch.cat([far * u.abs() * (1 + g.abs()), far * g.abs()], 1)
+    d = torch.cat([dg, du], 1)
+    th = h.abs() * (rz(g) + EPS16 * 1.01) + (g * u).abs() * FLUSH
+    h = torch.where(torch.isnan(dh), dh, h)
+    return (d, td + EPS16 * (d.abs() + td)), (h, th)
+
+
+def invert_ref(perm, n, end):
+    inv = torch.full((n,), -1, dtype=torch.int64)
+    for p in range(min(end, len(perm)) - 1, -1, -1):  # the lowest row is written last
+        a = int(perm[p])
+        if 0 <= a < n:
+            inv[a] = p
+    return inv.int()
+
+
+def combine_ref(y, inverse, k, weight=None, add=None):
+    """(out, tol without the result's rounding)."""
+    inv = inverse.long().view(-1, k)
+    has = (inv >= 0) & (inv < y.shape[0])
+    rows = y.to(F8)[inv.clamp(0, max(y.shape[0] - 1, 0))] if y.shape[0] else torch.zeros(*inv.shape, y.shape[1], dtype=F8)
+    rows = torch.where(has[:, :, None], rows, torch.zeros((), dtype=F8))
+    w = torch.ones(inv.shape, dtype=F8) if weight is None else torch.where(has, weight.to(F8), torch.zeros((), dtype=F8))
+    t = w[:, :, None] * rows
+    out, mag = t.sum(1), t.abs().sum(1)
+    if add is not None:
+        out, mag = out + add.to(F8), mag + add.to(F8).abs()
+    return out, (k + 1) * EPS32 * mag
+
+
+def dot_terms(H):
+    """Roundings that a sum over H elements by one wave adds up: eight elements a lane and 512, then six
+    steps of the wave, and the products' own."""
+    return 8 * ((H + 511) // 512) + 8
+
+
+def loss_ref(x, w, target, ignore=-100):
+    """(loss, tol, lse, tol, logits, tol, valid)."""
+    x, w = x.to(F8), w.to(F8)
+    H, V = x.shape[1], w.shape[0]
+    z = x @ w.t()
+    tz = 2 * EPS32 * H * (x.abs() @ w.abs().t())
+    lse = torch.logsumexp(z, 1)
+    valid = (target >= 0) & (target < V) & (target != ignore)
+    hit = z.gather(1, target.clamp(0, V - 1)[:, None])[:, 0]
+    m = z.max(1).values
+    # a sum of V positive terms: chains of 32 + 4 + 16 + V / 4096 additions; each term as exp above; the
+    # logarithm and the sum with the maximum
+    span = (m - z.min(1).values) + 2 * tz.max(1).values
+    tl = tz.max(1).values + (2 * span + 80 + V / 4096) * EPS32 + 4 * EPS32 * (m.abs() + lse.abs() + 1)
+    loss = torch.where(valid, lse - hit, torch.zeros((), dtype=F8))
+    t = torch.where(valid, tl + tz.gather(1, target.clamp(0, V - 1)[:, None])[:, 0] + EPS32 * (lse.abs() + hit.abs()),
+                    torch.zeros((), dtype=F8))
+    return loss, t, lse, tl, z, tz, valid
+
+
+def loss_grad_ref(d_loss, x, w, target, ignore=-100):
+    """((dx, tol), (dw, tol)) without the results' roundings."""
+    _, _, lse, tl, z, tz, valid = loss_ref(x, w, target, ignore)
+    T, V = z.shape
+    a = torch.where(valid, d_loss.to(F8), torch.zeros((), dtype=F8))
+    p = torch.exp(z - lse[:, None])
+    e = torch.zeros_like(p)
+    rows = torch.nonzero(valid)[:, 0]
+    e[rows, target[rows]] = 1.0
+    d = a[:, None] * (p - e)
+    rel = tz + tl[:, None] + (2 * (z - lse[:, None]).abs() + 8) * EPS32
+    td = a.abs()[:, None] * (p * rel * 1.01 + EPS32 * (p + e))
+    td = td + EPS16 * (d.abs() + td) + EPS32 * d.abs()
+    x, w = x.to(F8), w.to(F8)
+    dx, dw = d @ w, d.t() @ x
+    tx = td @ w.abs() + 2 * EPS32 * V * ((d.abs() + td) @ w.abs())
+    tw = td.t() @ x.abs() + 2 * EPS32 * T * ((d.abs() + td).t() @ x.abs())
+    return (dx, tx), (dw, tw)
