@@ -295,12 +295,13 @@ size_t moe_cross_entropy_workspace_size(const moe_loss_t* d);
 moe_status_t moe_cross_entropy(const moe_loss_t* d, const void* x, const void* w, const int64_t* target, float* loss,
                                float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* dz[t][v] = d_loss[t] (exp(z[t][v] - lse[t]) - (v == target[t])), rounded to bf16;
- * dx[t] = sum_v dz[t][v] w[v], dw[v] = sum_t dz[t][v] x[t].  lse as the forward call
+/* dz[t][v] = exp(z[t][v] - lse[t]) - (v == target[t]), rounded to bf16; dx[t] =
+ * d_loss[t] sum_v dz[t][v] w[v], dw[v] = m sum_t dz[t][v] r[t] with m the d_loss
+ * of largest magnitude of the tokens that have a target and r[t] = x[t] d_loss[t] / m, rounded to bf16.  lse as the forward call
  * gave it, d_loss fp32 [rows]; dx bf16 or fp32 [rows][ld] or not given, dw bf16 or
  * fp32 [V][H] or NULL.  The vocabulary goes by in pieces; the workspace
- * (moe_cross_entropy_grad_workspace_size bytes) holds one piece's dz and the sums of
- * dx. */
+ * (moe_cross_entropy_grad_workspace_size bytes) holds one piece's dz, the sums of
+ * dx and r. */
 size_t moe_cross_entropy_grad_workspace_size(const moe_loss_t* d);
 moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, const void* x, const void* w,
                                     const int64_t* target, const float* lse, moe_mat_t dx, moe_dtype_t dx_type, void* dw,

@@ -65,7 +65,7 @@ int64_t op_tile_units(OpKind kind, const Groups& g) {
 }
 
 hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, const void* b, const Scales& sc,
-                          void* out, bool fp32, hipStream_t s) {
+                          void* out, bool fp32, hipStream_t s, const float* factor) {
   TileArgs t{};
   t.g = g;
   t.a = (const char*)a;
@@ -73,6 +73,7 @@ hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, 
   t.sc = sc;
   t.out = out;
   t.fp32 = fp32;
+  t.factor = factor;
   t.nrow = (g.N + TB - 1) / TB;
   t.npan = ((kind == OP_NT ? g.N : g.K) + TB - 1) / TB;
   const unsigned grid = (unsigned)op_tile_units(kind, g);

@@ -58,9 +58,9 @@ struct Scales {
 
 enum OpKind { OP_NT = 0, OP_NN = 1, OP_TN = 2 };
 
-// Matrix-matrix kernels: y = x W^T, dx = dy W, dw = dy^T x.  i8: y from codes.
+// Matrix-matrix kernels: y = x W^T, dx = dy W, dw = dy^T x (times *factor, if given).  i8: y from codes.
 hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, const void* b, const Scales& sc,
-                          void* out, bool fp32, hipStream_t s);
+                          void* out, bool fp32, hipStream_t s, const float* factor = nullptr);
 // Matrix-vector kernel for few rows an expert: y = x W^T.  quantize: x is bf16,
 // w int8, and every workgroup quantises its rows itself.
 hipError_t launch_op_skinny(bool i8, bool quantize, const Groups& g, const void* x, const void* w, const Scales& sc, void* y,
@@ -157,7 +157,7 @@ constexpr int64_t kLossPieceBytes = 64 << 20;
 constexpr int kLossPieceColumns = 2048;
 struct LossPlan {
   int piece, slice, slices;
-  size_t d_bytes, bytes;
+  size_t d_bytes, part_bytes, x_bytes, bytes;
 };
 LossPlan loss_plan(int64_t rows, int V, int H);
 size_t loss_workspace(int64_t rows, int V);

@@ -26,6 +26,7 @@ struct TileArgs {
   int fp32;
   int npan;    // tiles along the second output dimension
   int nrow;    // TN: tiles along n
+  const float* factor;  // TN: the results are multiplied by it (NULL: not)
 };
 
 // Transfers go through range-checked buffer descriptors: a lane whose offset
@@ -623,6 +624,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       }
     }
   }
+  const float factor = KIND == OP_TN && p.factor ? *p.factor : 1.0f;
   // 32 x 64 results at a time through a part of the LDS of the wave's own, then 16 bytes a lane
   float* stage = (float*)(lds + HU) + wave * (32 * 64);
   auto write = [&](auto type) {
@@ -645,7 +647,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
             if constexpr (I8)
               v = (float)acc[h][b][j][r] * (s_scale[row0 + row] * ws[j]) + bi[j];
             else
-              v = acc[h][b][j][r];
+              v = KIND == OP_TN ? acc[h][b][j][r] * factor : acc[h][b][j][r];
             if constexpr (sizeof(T) == 4)
               st[row * 64 + 32 * j + l32] = v;
             else

@@ -402,6 +402,7 @@ def cross_entropy_grad(d_loss: torch.Tensor, x: torch.Tensor, w: torch.Tensor, t
                        stream=None) -> dict:
     """moe_cross_entropy_grad: the gradients of the loss of :func:`cross_entropy` as a dict ``x`` and ``w``
     (each in its dtype, left out where that is None), from d_loss (fp32 [tokens]) and the lse that the
-    forward call gave.  The gradient of a logit is rounded to bf16 before the products."""
+    forward call gave.  The gradient of a logit is rounded to bf16 before the products, without d_loss;
+    where the tokens' d_loss differ, so are the rows of x times their share of the largest one."""
     return _call(stream, _ops.cross_entropy_grad, d_loss, x, w, targets, lse, ignore_index,
                  None if dx_dtype is None else _fp32(dx_dtype), None if dw_dtype is None else _fp32(dw_dtype), workspace)

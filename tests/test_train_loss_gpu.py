@@ -67,6 +67,21 @@ def test_several_pieces():
     close(g["w"], dw, tw + EPS32 * dw.abs(), "w")
 
 
+@pytest.mark.parametrize("c", [1 / 999, 1.0039, -3e-5])
+def test_a_common_weight_is_not_rounded(c):
+    """A d_loss that all tokens share (a mean's 1 / n) scales the gradients: nothing but fp32 products of the
+    results is rounded by it, though bf16 holds none of these values."""
+    T, V, H = 300, 513, 128
+    x, w, t = (v.cuda() for v in inputs(T, V, H))
+    lse = ops.cross_entropy(x, w, t)[1]
+    one, other = (ops.cross_entropy_grad(torch.full((T,), v, device="cuda"), x, w, t, lse, dx_dtype=F32, dw_dtype=F32)
+                  for v in (1.0, c))
+    c32 = torch.tensor(c, dtype=F32).to(F8)
+    for k in ("x", "w"):
+        want = one[k].cpu().to(F8) * c32
+        close(other[k], want, 2 * EPS32 * want.abs(), k)
+
+
 @pytest.mark.parametrize("ignore", [-100, 3, 0])
 def test_ignored_tokens(ignore):
     """Tokens without a target have no part, whatever their logits are."""

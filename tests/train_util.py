@@ -110,12 +110,17 @@ def loss_grad_ref(d_loss, x, w, target, ignore=-100):
     e = torch.zeros_like(p)
     rows = torch.nonzero(valid)[:, 0]
     e[rows, target[rows]] = 1.0
-    d = a[:, None] * (p - e)
+    # the kernel's d is p - e in bf16: p off by the logit's and the log-sum-exp's errors and its own
+    # exponential, then a difference, then the rounding
     rel = tz + tl[:, None] + (2 * (z - lse[:, None]).abs() + 8) * EPS32
-    td = a.abs()[:, None] * (p * rel * 1.01 + EPS32 * (p + e))
-    td = td + EPS16 * (d.abs() + td) + EPS32 * d.abs()
+    u = torch.where(valid[:, None], p - e, torch.zeros((), dtype=F8))
+    tu = torch.where(valid[:, None], p * rel * 1.01 + EPS32 * (p + e), torch.zeros((), dtype=F8))
+    tu = tu + EPS16 * (u.abs() + tu)
     x, w = x.to(F8), w.to(F8)
-    dx, dw = d @ w, d.t() @ x
-    tx = td @ w.abs() + 2 * EPS32 * V * ((d.abs() + td) @ w.abs())
-    tw = td.t() @ x.abs() + 2 * EPS32 * T * ((d.abs() + td).t() @ x.abs())
+    dx, dw = (a[:, None] * u) @ w, (a[:, None] * u).t() @ x
+    tx = a.abs()[:, None] * (tu @ w.abs() + (2 * V + 2) * EPS32 * ((u.abs() + tu) @ w.abs()))
+    # dw: rows x a / max |a|, two roundings of fp32 and one to bf16, which is none where all a are the same
+    same = bool((a[valid].abs() == a.abs().max()).all()) if bool(valid.any()) else True
+    row = a.abs()[:, None] * x.abs()
+    tw = tu.t() @ row + ((0 if same else 1.01 * EPS16) + (2 * T + 4) * EPS32) * ((u.abs() + tu).t() @ row)
     return (dx, tx), (dw, tw)
