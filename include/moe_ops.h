@@ -206,6 +206,32 @@ moe_status_t moe_gated_matmul(const moe_groups_t* g, const void* x, const void* 
 moe_status_t moe_gated_matmul_grad(const moe_groups_t* g, const void* dy, const void* w, moe_mat_t gate_up,
                                    moe_mat_t d_gate_up, void* h, hipStream_t stream);
 
+/* A gated feed-forward block: y[p] = h[p] . D_e^T of H columns with h of I features from
+ * moe_gated_matmul.  K, H and I multiples of 8, K and I at most 16384, 2 I and H at most
+ * 2^20; the other fields as in moe_groups_t. */
+typedef struct {
+  int64_t rows, x_rows;
+  int64_t ldx;            /* of x */
+  int64_t ld_dy;          /* of dy, >= H */
+  int32_t E, I, K, H;
+  int32_t top_k;
+  const int32_t* offsets;
+  const int32_t* perm;
+} moe_feed_forward_t;
+
+/* Its gradients from dy, with moe_gated_matmul_grad's d_gate_up and h:
+ *   dx = d_gate_up . W_e (of each grouped row, as moe_grouped_matmul_grad_input),
+ *   dw_gate_up = d_gate_up^T x[row(p)],  dw_down = dy^T h (as ..._grad_weight).
+ * dy bf16 [rows][ld_dy], x bf16 [x_rows][ldx], w_gate_up bf16 [E][2 I][K], w_down bf16
+ * [E][H][I], gate_up bf16 [rows][ld] of 2 I columns as the forward call kept it, dx bf16
+ * [rows][ld], dw_gate_up and dw_down in dw_type, of the weights' shapes.  workspace:
+ * moe_feed_forward_grad_workspace_size bytes, which hold d_gate_up, h and, where few experts
+ * have long groups, parts of the weight gradients. */
+size_t moe_feed_forward_grad_workspace_size(const moe_feed_forward_t* d);
+moe_status_t moe_feed_forward_grad(const moe_feed_forward_t* d, const void* dy, const void* x, const void* w_gate_up,
+                                   const void* w_down, moe_mat_t gate_up, moe_mat_t dx, void* dw_gate_up, void* dw_down,
+                                   moe_dtype_t dw_type, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------------ combine */
 
 /* inverse[a] = the row p with perm[p] == a, the lowest of several, for the
@@ -276,7 +302,7 @@ moe_status_t moe_clip_grads(const moe_tensor_t* tensors, int32_t count, float ma
 /* ------------------------------------------------------------ cross entropy */
 
 /* Tokens against a vocabulary: 1 <= V <= 2^20, H a multiple of 8, 8 <= H <= 16384,
- * ldx a multiple of 8, H <= ldx <= 2^20, rows < 2^31, and fewer than 2^22 tiles of
+ * ldx a multiple of 8, H <= ldx <= 2^20, rows < 2^31, and at most 2^21 tiles of
  * 256 x 256 in a matrix of as many rows and of V, or of H, columns.  A token whose target is ignore_index or lies outside
  * [0, V) has no target: its loss is 0 and it has no part in the gradients. */
 typedef struct {

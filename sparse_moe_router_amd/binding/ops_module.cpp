@@ -566,6 +566,39 @@ PyObject* gated_matmul_grad(PyObject*, Args a, Py_ssize_t n) {
   });
 }
 
+// dy, x, w_gate_up, w_down, gate_up, offsets, perm, top_k, dw fp32, workspace
+PyObject* feed_forward_grad(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    Call c;
+    const Tensor& dy = c.tensor(a[0], {BF16}, 2, "dy");
+    const Tensor& x = c.tensor(a[1], {BF16}, 2, "x");
+    const Tensor& w = c.tensor(a[2], {BF16}, 3, "w_gate_up");
+    if (w.size(1) % 2) value_error("w_gate_up must have the rows of two matrices, got " + shape_of(w));
+    moe_feed_forward_t d{};
+    d.E = dim32(w.size(0), "w_gate_up"), d.I = dim32(w.size(1) / 2, "w_gate_up"), d.K = dim32(w.size(2), "w_gate_up");
+    d.H = dim32(dy.size(1), "dy");
+    const int64_t I2 = 2 * (int64_t)d.I;
+    const void* wp = c.flat(a[2], {BF16}, {d.E, I2, d.K}, "w_gate_up");
+    const void* wd = c.flat(a[3], {BF16}, {d.E, d.H, d.I}, "w_down");
+    const moe_mat_t dym = c.rows(a[0], {BF16}, -1, d.H, "dy"), xm = c.rows(a[1], {BF16}, -1, d.K, "x");
+    d.rows = dy.size(0), d.x_rows = x.size(0), d.ldx = xm.ld, d.ld_dy = dym.ld;
+    const moe_mat_t pm = c.rows(a[4], {BF16}, d.rows, I2, "gate_up");
+    moe_groups_t g{};
+    g.rows = d.rows, g.E = d.E;
+    set_groups(c, &g, a[5], a[6], a[7]);
+    d.offsets = g.offsets, d.perm = g.perm, d.top_k = g.top_k;
+    const auto type = out_type(a[8]);
+    c.begin();
+    Tensor dx = c.empty({d.rows, d.K}, BF16), dgu = c.empty({d.E, I2, d.K}, type), dwd = c.empty({d.E, d.H, d.I}, type), wk;
+    size_t have = 0;
+    void* wkp = workspace(c, a[9], moe_feed_forward_grad_workspace_size(&d), &wk, &have);
+    check(moe_feed_forward_grad(&d, dym.data, xm.data, wp, wd, pm, moe_mat_t{dx.data_ptr(), d.K}, dgu.data_ptr(),
+                                dwd.data_ptr(), dt(dgu), wkp, have, c.stream),
+          "moe_feed_forward_grad");
+    return Py_BuildValue("{sNsNsN}", "x", wrap(dx), "w_gate_up", wrap(dgu), "w_down", wrap(dwd));
+  });
+}
+
 // group offsets of any number of experts; their number
 const int32_t* any_offsets(Call& c, PyObject* o, int32_t* E) {
   if (!given(o)) return nullptr;
@@ -858,6 +891,7 @@ PyMethodDef methods[] = {FAST(grouped_matmul),
                          FAST(block_merge_grad),
                          FAST(gated_matmul),
                          FAST(gated_matmul_grad),
+                         FAST(feed_forward_grad),
                          FAST(invert_permutation),
                          FAST(combine),
                          FAST(combine_grad),

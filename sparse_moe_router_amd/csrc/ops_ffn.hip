@@ -1,0 +1,109 @@
+// The products behind k_gated_grad in the backward pass of a gated feed-forward
+// block (gfx950):
+//   dx = d_pre W_gu,  dW_gu = d_pre^T x[row],  dW_d = dy^T h
+// in one launch: none needs another's result, and the tiles of the later ones
+// fill the compute units that the last tiles of the earlier ones leave (in three
+// launches each waits for the slowest tile before it).  The rows' gradient comes
+// first, whose tiles are the longest of most blocks.  Weight gradients with few
+// tiles (few experts) are cut along their rows; the parts are added in a fixed
+// order by a second launch.
+#include "ops_sum.h"
+#include "ops_tile.h"
+
+namespace moe {
+namespace {
+
+struct FfnTiles {
+  TileArgs dx, gu, down;
+  int dx_units, gu_units;  // multiples of 8: a workgroup's XCD is that of its unit
+};
+
+template <int GX>
+__global__ __launch_bounds__(512, 1) void k_ffn_products(FfnTiles a) {
+  __shared__ u32x4_t lds[10 * HU];
+  int b = blockIdx.x;
+  if (b < a.dx_units) {
+    row_tile<OP_NN, false, GX_ROWS>(a.dx, lds);
+    return;
+  }
+  b -= a.dx_units;
+  if (b < a.gu_units)
+    wgrad_tile<GX>(a.gu, b, lds);
+  else
+    wgrad_tile<GX_ROWS>(a.down, b - a.gu_units, lds);
+}
+
+Groups gu_groups(const FfnArgs& a) {
+  Groups g = a.g;
+  g.ldy = a.ld_dpre;
+  return g;
+}
+Groups down_groups(const FfnArgs& a) {
+  return Groups{a.g.rows, a.g.rows, a.ld_h, a.ld_dy, a.g.E, a.H, a.I, 1, a.g.offsets, nullptr};
+}
+Groups dx_groups(const FfnArgs& a) {
+  Groups g = gu_groups(a);
+  g.ldx = a.ld_dx;
+  g.perm = nullptr;
+  return g;
+}
+int64_t dx_units(const FfnArgs& a) { return row_tile_units(a.g, (a.g.K + TB - 1) / TB); }
+
+TileArgs weight_tiles(const Groups& g, const void* dy, const void* x, void* out, bool fp32, int splits) {
+  TileArgs t{};
+  t.g = g;
+  t.a = (const char*)dy;
+  t.b = (const char*)x;
+  t.out = out;
+  t.fp32 = fp32;
+  t.nrow = (g.N + TB - 1) / TB;
+  t.npan = (g.K + TB - 1) / TB;
+  t.splits = splits;
+  return t;
+}
+
+}  // namespace
+
+// Parts: as many as the 256 workgroups that run at a time hold, of at least four steps of 64 rows of a
+// group of average size.
+int ffn_splits(const FfnArgs& a) {
+  const int64_t units = wgrad_units(a.g, 1) + wgrad_units(down_groups(a), 1);
+  const int64_t most = a.g.rows / (256 * (int64_t)a.g.E);
+  int64_t n = kChainGroups / units;
+  n = n < most ? n : most;
+  return n > 1 ? (int)n : 1;
+}
+size_t ffn_split_bytes(const FfnArgs& a) {
+  const int n = ffn_splits(a);
+  return n > 1 ? (size_t)n * a.g.E * ((size_t)a.g.N * a.g.K + (size_t)a.H * a.I) * 4 : 0;
+}
+int64_t ffn_units(const FfnArgs& a) {
+  const int n = ffn_splits(a);
+  return dx_units(a) + wgrad_units(a.g, n) + wgrad_units(down_groups(a), n);
+}
+
+hipError_t launch_ffn_products(const FfnArgs& a, float* part, hipStream_t s) {
+  const int n = ffn_splits(a);
+  const int64_t gu_size = (int64_t)a.g.E * a.g.N * a.g.K, down_size = (int64_t)a.g.E * a.H * a.I;
+  float* down_part = part + n * gu_size;
+  FfnTiles f{};
+  f.dx.g = dx_groups(a);
+  f.dx.a = (const char*)a.d_pre;
+  f.dx.b = (const char*)a.w_gate_up;
+  f.dx.out = a.dx;
+  f.dx.npan = (a.g.K + TB - 1) / TB;
+  f.gu = weight_tiles(gu_groups(a), a.d_pre, a.x, n > 1 ? part : a.dw_gate_up, n > 1 || a.dw32, n);
+  f.down = weight_tiles(down_groups(a), a.dy, a.h, n > 1 ? down_part : a.dw_down, n > 1 || a.dw32, n);
+  f.dx_units = a.g.rows > 0 ? (int)dx_units(a) : 0;
+  f.gu_units = (int)wgrad_units(a.g, n);
+  const dim3 grid((unsigned)(f.dx_units + f.gu_units + wgrad_units(f.down.g, n))), block(512);
+  const Launch lc{s, nullptr, nullptr};
+  hipError_t e = !a.g.perm             ? launch(lc, k_ffn_products<GX_ROWS>, grid, block, f)
+                 : rows_far(a.g, 2) ? launch(lc, k_ffn_products<GX_FAR>, grid, block, f)
+                                       : launch(lc, k_ffn_products<GX_INDEX>, grid, block, f);
+  if (e != hipSuccess || n == 1) return e;
+  e = launch_sum_parts(part, n, gu_size, nullptr, a.dw_gate_up, a.dw32, s);
+  return e != hipSuccess ? e : launch_sum_parts(down_part, n, down_size, nullptr, a.dw_down, a.dw32, s);
+}
+
+}  // namespace moe

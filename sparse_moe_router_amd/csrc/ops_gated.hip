@@ -18,9 +18,6 @@ namespace {
 
 constexpr int GATED_COLS = TB / 2;  // features of a tile
 
-// Wave-private LDS: 8 KB.
-__device__ __forceinline__ char* wave_stage(u32x4_t* lds, const TileOut& o) { return (char*)(lds + o.wave * 512); }
-
 struct GatedEpi {
   static constexpr bool kGated = true;
   uint16_t* h;
@@ -31,29 +28,33 @@ struct GatedEpi {
   template <int RB0, int RB1, class ACC>
   __device__ __forceinline__ void tile(const TileArgs& p, const TileOut& o, ACC& acc, u32x4_t* lds) const {
     const int n = p.g.N, col0 = o.c0 + 32 * o.wn;
-    uint16_t* st = (uint16_t*)wave_stage(lds, o);  // [h, gate, up][32 rows][32 columns]
-    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& g, const f32x16_t& u) {
+    uint16_t* st = (uint16_t*)epi_stage(lds, o);  // 32 rows x 32 columns, of h, or of gate and up
+    // 16 bytes a lane from the stage's part `from` to columns `at` of out
+    auto put = [&](int row0, int from, uint16_t* out, int64_t ld, int at0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = i * 64 + o.lane, row = c >> 2, at = (c & 3) * 8;
+        if (row0 + row < o.rows && col0 + at < n)
+          *(u32x4_t*)(out + (o.p0 + row0 + row) * ld + at0 + col0 + at) = *(const u32x4_t*)(st + from + row * 32 + at);
+      }
+    };
+    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& g, const f32x16_t& u) __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        st[block_row(r, o.lane) * 32 + (o.lane & 31)] = (uint16_t)f32_to_bf16(silu(g[r]) * u[r]);
+      wave_sync();
+      put(row0, 0, h, ldh, 0);
+      wave_sync();
+      if (!pre) return;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int at = block_row(r, o.lane) * 32 + (o.lane & 31);
-        st[at] = (uint16_t)f32_to_bf16(silu(g[r]) * u[r]);
-        if (pre) {
-          st[1024 + at] = (uint16_t)f32_to_bf16(g[r]);
-          st[2048 + at] = (uint16_t)f32_to_bf16(u[r]);
-        }
+        st[at] = (uint16_t)f32_to_bf16(g[r]);
+        st[1024 + at] = (uint16_t)f32_to_bf16(u[r]);
       }
       wave_sync();
-#pragma unroll
-      for (int c = o.lane; c < 128; c += 64) {  // 16 bytes a lane
-        const int row = c >> 2, at = (c & 3) * 8, col = col0 + at;
-        if (row0 + row >= o.rows || col >= n) continue;
-        const int64_t grow = o.p0 + row0 + row;
-        *(u32x4_t*)(h + grow * ldh + col) = *(const u32x4_t*)(st + row * 32 + at);
-        if (pre) {
-          *(u32x4_t*)(pre + grow * ldp + col) = *(const u32x4_t*)(st + 1024 + row * 32 + at);
-          *(u32x4_t*)(pre + grow * ldp + n + col) = *(const u32x4_t*)(st + 2048 + row * 32 + at);
-        }
-      }
+      put(row0, 0, pre, ldp, 0);
+      put(row0, 1024, pre, ldp, n);
       wave_sync();
     });
   }
@@ -93,45 +94,42 @@ struct GatedGradEpi {
   template <int RB0, int RB1, class ACC>
   __device__ __forceinline__ void tile(const TileArgs& p, const TileOut& o, ACC& acc, u32x4_t* lds) const {
     const int n = p.g.K;
-    float* st = (float*)wave_stage(lds, o);  // [32 rows][64 columns]
-    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) {
+    float* st = (float*)epi_stage(lds, o);
+    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) __attribute__((always_inline)) {
       // columns 0..31 of the stage: the wave's block of the first half, 32..63: of the second
+      const int chunk = o.lane & 7, col = o.c0 + 128 * (chunk >> 2) + 32 * o.wn + (chunk & 3) * 8;
       u32x4_t g[4], u[4];
       bool in[4];
       int64_t grow[4];
-      int col[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = i * 8 + (o.lane >> 3), at = (o.lane & 7) * 8;
-        col[i] = o.c0 + 128 * (at >> 5) + 32 * o.wn + (at & 31);
+        const int row = i * 8 + (o.lane >> 3);
         grow[i] = o.p0 + row0 + row;
-        in[i] = row0 + row < o.rows && col[i] < n;
+        in[i] = row0 + row < o.rows && col < n;
         g[i] = u[i] = u32x4_t{0, 0, 0, 0};
         if (in[i]) {
-          g[i] = *(const u32x4_t*)(pre + grow[i] * ldp + col[i]);
-          u[i] = *(const u32x4_t*)(pre + grow[i] * ldp + n + col[i]);
+          g[i] = *(const u32x4_t*)(pre + grow[i] * ldp + col);
+          u[i] = *(const u32x4_t*)(pre + grow[i] * ldp + n + col);
         }
       }
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int at = block_row(r, o.lane) * 64 + (o.lane & 31);
-        st[at] = a0[r];
-        st[at + 32] = a1[r];
-      }
-      wave_sync();
+      for (int q = 0; q < 2; ++q) {
+        stage16(st, q, o.lane, a0, a1);
+        wave_sync();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4_t* s = (const f32x4_t*)(st + (i * 8 + (o.lane >> 3)) * 64 + (o.lane & 7) * 8);
-        const f32x4_t x = s[0], y = s[1];
-        const float dh[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        u32x4_t dg, du, v;
-        gate_grad(dh, g[i], u[i], &dg, &du, &v);
-        if (!in[i]) continue;
-        *(u32x4_t*)(d_pre + grow[i] * ldd + col[i]) = dg;
-        *(u32x4_t*)(d_pre + grow[i] * ldd + n + col[i]) = du;
-        *(u32x4_t*)(h + grow[i] * ldh + col[i]) = v;
+        for (int k = 0; k < 2; ++k) {
+          const int i = 2 * q + k, row = k * 8 + (o.lane >> 3);
+          const f32x4_t x = *staged(st, row, 2 * chunk), y = *staged(st, row, 2 * chunk + 1);
+          const float dh[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+          u32x4_t dg, du, v;
+          gate_grad(dh, g[i], u[i], &dg, &du, &v);
+          if (!in[i]) continue;
+          *(u32x4_t*)(d_pre + grow[i] * ldd + col) = dg;
+          *(u32x4_t*)(d_pre + grow[i] * ldd + n + col) = du;
+          *(u32x4_t*)(h + grow[i] * ldh + col) = v;
+        }
+        wave_sync();
       }
-      wave_sync();
     });
   }
 };

@@ -39,33 +39,41 @@ __global__ __launch_bounds__(512, 1) void k_op_rows(TileArgs p) {
   __shared__ u32x4_t lds[10 * HU];  // 160 KB
   row_tile<KIND, I8, GX>(p, lds);
 }
+template <OpKind KIND>
+__global__ __launch_bounds__(512, 1) void k_op_rows_chain(TileArgs p) {
+  __shared__ u32x4_t lds[10 * HU];
+  row_chain<KIND>(p, lds);
+}
 
-// Weight gradients (TN): a workgroup per expert and 256 x 256 tile of dw, in
-// eight equal runs, one for each XCD: an expert's tiles share dy and x in one
-// L2.
+// Weight gradients (TN).
 template <int GX>
 __global__ __launch_bounds__(512, 1) void k_op_wgrad(TileArgs p) {
-  __shared__ u32x4_t lds[8 * HU];
-  __shared__ int32_t gidx[GX == GX_ROWS ? 1 : GI];  // 32 KB
-  const int per = p.nrow * p.npan;
-  const int run = (p.g.E * per + 7) / 8, unit = (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3);
-  if (unit >= p.g.E * per) return;
-  const int e = unit / per, tile = unit % per;
-  const Range r = group_range(p.g, e);
-  tile_product<OP_TN, false, 2, 2, GX, false>(p, e, uniform64(r.lo), 0, uniform64(r.size()), tile / p.npan, tile % p.npan, lds,
-                                       gidx);
+  __shared__ u32x4_t lds[10 * HU];
+  wgrad_tile<GX>(p, blockIdx.x, lds);
+}
+// Of one matrix, whose units all take the same time: 32 workgroups of an XCD take its units in turn.
+__global__ __launch_bounds__(512, 1) void k_op_wgrad_chain(TileArgs p) {
+  __shared__ u32x4_t lds[10 * HU];
+  int unit = blockIdx.x;
+  TileJob t;
+  if (wgrad_unit(p, unit, &t) < 0) return;
+  tile_product<OP_TN, false, 2, 2, GX_ROWS, false>(p, t, lds, nullptr, StoreEpi{},
+                                                   chain_next([&](TileJob& t) __attribute__((always_inline)) {
+                                                     unit += kChainGroups;
+                                                     return wgrad_unit(p, unit, &t) >= 0;
+                                                   }));
 }
 
 }  // namespace
 
 int64_t op_tile_units(OpKind kind, const Groups& g) {
   const int64_t pn = (g.N + TB - 1) / TB, pk = (g.K + TB - 1) / TB;
-  if (kind == OP_TN) return (g.E * pn * pk + 7) / 8 * 8;
+  if (kind == OP_TN) return wgrad_units(g, 1);
   return row_tile_units(g, kind == OP_NT ? pn : pk);
 }
 
 hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, const void* b, const Scales& sc,
-                          void* out, bool fp32, hipStream_t s, const float* factor) {
+                          void* out, bool fp32, hipStream_t s) {
   TileArgs t{};
   t.g = g;
   t.a = (const char*)a;
@@ -73,21 +81,25 @@ hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, 
   t.sc = sc;
   t.out = out;
   t.fp32 = fp32;
-  t.factor = factor;
   t.nrow = (g.N + TB - 1) / TB;
   t.npan = ((kind == OP_NT ? g.N : g.K) + TB - 1) / TB;
   const unsigned grid = (unsigned)op_tile_units(kind, g);
   const Launch lc{s, nullptr, nullptr};
   const bool far = rows_far(g, i8 ? 1 : 2);
-  const dim3 gr(grid), bl(512);
+  const bool chain = !i8 && !g.perm && (kind == OP_TN ? !g.offsets && grid > kChainGroups : takes_chain(g, grid));
+  const dim3 gr(chain ? (unsigned)kChainGroups : grid), bl(512);
   if (kind == OP_TN) {
+    if (chain) return launch(lc, k_op_wgrad_chain, gr, bl, t);
     if (!g.perm) return launch(lc, k_op_wgrad<GX_ROWS>, gr, bl, t);
     return far ? launch(lc, k_op_wgrad<GX_FAR>, gr, bl, t) : launch(lc, k_op_wgrad<GX_INDEX>, gr, bl, t);
   }
-  if (kind == OP_NN) return launch(lc, k_op_rows<OP_NN, false, GX_ROWS>, gr, bl, t);
+  if (kind == OP_NN)
+    return chain ? launch(lc, k_op_rows_chain<OP_NN>, gr, bl, t)
+                 : launch(lc, k_op_rows<OP_NN, false, GX_ROWS>, gr, bl, t);
   if (i8)
     return far ? launch(lc, k_op_rows<OP_NT, true, GX_FAR>, gr, bl, t)
                : launch(lc, k_op_rows<OP_NT, true, GX_ROWS>, gr, bl, t);
+  if (chain) return launch(lc, k_op_rows_chain<OP_NT>, gr, bl, t);
   return far ? launch(lc, k_op_rows<OP_NT, false, GX_FAR>, gr, bl, t)
              : launch(lc, k_op_rows<OP_NT, false, GX_ROWS>, gr, bl, t);
 }

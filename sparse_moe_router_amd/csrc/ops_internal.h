@@ -58,9 +58,9 @@ struct Scales {
 
 enum OpKind { OP_NT = 0, OP_NN = 1, OP_TN = 2 };
 
-// Matrix-matrix kernels: y = x W^T, dx = dy W, dw = dy^T x (times *factor, if given).  i8: y from codes.
+// Matrix-matrix kernels: y = x W^T, dx = dy W, dw = dy^T x.  i8: y from codes.
 hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, const void* b, const Scales& sc,
-                          void* out, bool fp32, hipStream_t s, const float* factor = nullptr);
+                          void* out, bool fp32, hipStream_t s);
 // Matrix-vector kernel for few rows an expert: y = x W^T.  quantize: x is bf16,
 // w int8, and every workgroup quantises its rows itself.
 hipError_t launch_op_skinny(bool i8, bool quantize, const Groups& g, const void* x, const void* w, const Scales& sc, void* y,
@@ -77,6 +77,21 @@ hipError_t launch_gated(const Groups& g, const void* x, const void* w, void* h, 
 hipError_t launch_gated_skinny(const Groups& g, const void* x, const void* w, void* h, void* pre, int64_t ldp,
                                hipStream_t s);
 int64_t gated_units(const Groups& g);
+// The gradients of a gated feed-forward block: of its rows and both weights, from d_pre and h.
+struct FfnArgs {
+  Groups g;  // of x and w_gate_up: N = 2 I
+  int I, H;
+  const void *dy, *x, *w_gate_up, *d_pre, *h;
+  int64_t ld_dy, ld_dpre, ld_h;
+  void *dx, *dw_gate_up, *dw_down;
+  int64_t ld_dx;
+  bool dw32;
+};
+// Parts that the reduction of each weight gradient is cut into, and their bytes of workspace.
+int ffn_splits(const FfnArgs& a);
+size_t ffn_split_bytes(const FfnArgs& a);
+int64_t ffn_units(const FfnArgs& a);
+hipError_t launch_ffn_products(const FfnArgs& a, float* part, hipStream_t s);
 // dy W through the gate: d_pre and h of g.K features.
 hipError_t launch_gated_grad(const Groups& g, const void* dy, const void* w, const void* pre, int64_t ldp, void* d_pre,
                              int64_t ldd, void* h, int64_t ldh, hipStream_t s);
@@ -153,11 +168,12 @@ struct LossArgs {
 // The gradient goes through the vocabulary in pieces whose d (bf16) takes at most kLossPieceBytes,
 // but at least kLossPieceColumns columns; dx is summed in `slices` buffers, each over `slice` columns
 // of a piece.
-constexpr int64_t kLossPieceBytes = 64 << 20;
+constexpr int64_t kLossPieceBytes = 256 << 20;
 constexpr int kLossPieceColumns = 2048;
 struct LossPlan {
   int piece, slice, slices;
-  size_t d_bytes, part_bytes, x_bytes, bytes;
+  int splits;  // parts of the reduction of dw
+  size_t d_bytes, part_bytes, x_bytes, dw_bytes, bytes;
 };
 LossPlan loss_plan(int64_t rows, int V, int H);
 size_t loss_workspace(int64_t rows, int V);

@@ -19,25 +19,24 @@
 // of which 0.17% is the rounding of the results).  dx takes d_loss in fp32 with
 // its last sum; dW takes the largest d_loss in its epilogue, and the token's
 // share of that, exactly 1 for a mean, into the bf16 copy of x that it reads.
+#include "ops_sum.h"
 #include "ops_tile.h"
 
 namespace moe {
 namespace {
 
-constexpr int ST_LD = 68;  // floats from a staged row to the next: rows 16 bytes of banks apart
-
-// 32 x 64 results of a wave, columns 0..31 of its block of the first column half, 32..63 of the second.
-__device__ __forceinline__ void stage_block(float* st, int ld, const TileOut& o, const f32x16_t& a0, const f32x16_t& a1) {
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int at = block_row(r, o.lane) * ld + (o.lane & 31);
-    st[at] = a0[r];
-    st[at + 32] = a1[r];
-  }
-}
+constexpr float LOG2E = 1.44269504088896340736f;
 
 // exp(x - m), 0 where both are -inf.
 __device__ __forceinline__ float exp_from(float x, float m) { return x == -INFINITY ? 0.0f : __expf(x - m); }
+
+// The value of lane i ^ 1, i ^ 2 of each four.
+__device__ __forceinline__ float quad_xor1(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float quad_xor2(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
+}
 
 struct LseEpi {
   static constexpr bool kGated = false;
@@ -48,37 +47,76 @@ struct LseEpi {
 
   template <int RB0, int RB1, class ACC>
   __device__ __forceinline__ void tile(const TileArgs& p, const TileOut& o, ACC& acc, u32x4_t* lds) const {
-    float* st = (float*)lds + o.wave * (32 * ST_LD);
-    float2* sums = (float2*)((float*)lds + 8 * 32 * ST_LD);  // [wn][256]
-    const int side = o.lane & 1;                             // two lanes a row: one for each column half
-    const int col = o.c0 + 64 * o.wn + 32 * side, n = p.g.N - col;
-    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) {
-      const int row = row0 + (o.lane >> 1);
-      const bool in = row < o.rows;
-      const int64_t t = in ? target[o.p0 + row] - col : -1;
-      stage_block(st, ST_LD, o, a0, a1);
-      wave_sync();
-      const float* at = st + (o.lane >> 1) * ST_LD + 32 * side;
-      float v[32];
+    float* st = (float*)epi_stage(lds, o);
+    const int side = o.lane & 3;  // four lanes a row, 16 columns each
+    const int col = o.c0 + 64 * o.wn + 16 * side, n = p.g.N - col;
+    const bool whole = o.c0 + TB <= p.g.N;  // uniform
+    constexpr int NB = RB0 + RB1;
+    float2 mine[NB][2];  // of the lane's row in each half block
+    int b = 0;
+    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) __attribute__((always_inline)) {
+      int64_t t[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const f32x4_t q = *(const f32x4_t*)(at + 4 * i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[4 * i + k] = 4 * i + k < n ? q[k] : -INFINITY;
+      for (int q = 0; q < 2; ++q) {
+        const int row = row0 + 16 * q + (o.lane >> 2);
+        t[q] = row < o.rows ? target[o.p0 + row] - col : -1;
       }
-      if (t >= 0 && t < 32 && t < n) hit[o.p0 + row] = at[t];
-      float m = v[0];
+      // both halves are read before either is reduced: their chains of exchanges overlap
+      float v[2][16];
+      const int row = o.lane >> 2;
 #pragma unroll
-      for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
-      m = fmaxf(m, __shfl_xor(m, 1, 64));
-      float s = 0.0f;
+      for (int q = 0; q < 2; ++q) {
+        stage16(st, q, o.lane, a0, a1);
+        wave_sync();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s += exp_from(v[i], m);
-      s += __shfl_xor(s, 1, 64);
-      if (side == 0) sums[o.wn * TB + row] = float2{m, s};
-      wave_sync();
+        for (int i = 0; i < 4; ++i) {
+          const f32x4_t x = *staged(st, row, 4 * side + i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[q][4 * i + k] = x[k];
+        }
+        if (t[q] >= 0 && t[q] < 16 && t[q] < n)
+          hit[o.p0 + row0 + 16 * q + row] = ((const float*)staged(st, row, 4 * side + ((int)t[q] >> 2)))[t[q] & 3];
+        wave_sync();
+      }
+      if (!whole)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) v[q][i] = i < n ? v[q][i] : -INFINITY;
+      float m[2], s[2] = {0.0f, 0.0f}, shift[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        m[q] = v[q][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) m[q] = fmaxf(m[q], v[q][i]);
+        m[q] = fmaxf(m[q], quad_xor1(m[q]));
+        m[q] = fmaxf(m[q], quad_xor2(m[q]));
+        // exp(v - m) = 2^(v log2(e) - m log2(e)); of -inf 0 even where all are
+        shift[q] = -fmaxf(m[q], -2e38f) * LOG2E;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) s[q] += __builtin_amdgcn_exp2f(fmaf(v[q][i], LOG2E, shift[q]));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        s[q] += quad_xor1(s[q]);
+        s[q] += quad_xor2(s[q]);
+        mine[b][q] = float2{m[q], s[q]};
+      }
+      ++b;
     });
-    __syncthreads();
+    bar();  // the stages are free
+    float2* sums = (float2*)(lds + EPI_AT);  // [wn][256]
+    b = 0;
+    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t&, const f32x16_t&) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (side == 0) sums[o.wn * TB + row0 + 16 * q + (o.lane >> 2)] = mine[b][q];
+      ++b;
+    });
+    wait_vm<63>();
+    bar();
     if (o.tid >= o.rows) return;
     float m = -INFINITY, s = 0.0f;
 #pragma unroll
@@ -89,9 +127,13 @@ struct LseEpi {
   }
 };
 
+template <bool CHAIN>
 __global__ __launch_bounds__(512, 1) void k_loss_logits(TileArgs p, LseEpi epi) {
   __shared__ u32x4_t lds[10 * HU];
-  row_tile<OP_NT, false, GX_ROWS>(p, lds, epi);
+  if constexpr (CHAIN)
+    row_chain<OP_NT>(p, lds, epi);
+  else
+    row_tile<OP_NT, false, GX_ROWS>(p, lds, epi);
 }
 
 // Joins the panels of 16 rows, 16 threads a row.
@@ -132,33 +174,59 @@ __device__ __forceinline__ float larger(float a, float b) {
 
 // scale[t] = d_loss[t], 0 for a token without a target; *most = the one of largest magnitude, with its
 // sign, so that a d_loss that all tokens share is 1 of it.
+__device__ __forceinline__ float scale_of(const float* d_loss, const int64_t* target, int64_t ignore, int V, int64_t t) {
+  const int64_t g = target[t];
+  return g >= 0 && g < V && g != ignore ? d_loss[t] : 0.0f;
+}
+template <int WAVES>
+__device__ __forceinline__ float largest(float m, float* lds) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) m = larger(m, __shfl_xor(m, d, 64));
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
+  __syncthreads();
+  for (int i = 0; i < WAVES; ++i) m = larger(m, lds[i]);
+  return m;
+}
 __global__ __launch_bounds__(1024) void k_loss_scale(const float* d_loss, const int64_t* target, int64_t ignore, int V,
                                                      int64_t rows, float* scale, float* most) {
   __shared__ float lds[16];
   float m = 0.0f;
 #pragma unroll 4
   for (int64_t t = threadIdx.x; t < rows; t += 1024) {
-    const int64_t g = target[t];
-    const float a = g >= 0 && g < V && g != ignore ? d_loss[t] : 0.0f;
+    const float a = scale_of(d_loss, target, ignore, V, t);
     scale[t] = a;
     m = larger(m, a);
   }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) m = larger(m, __shfl_xor(m, d, 64));
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  for (int i = 1; i < 16; ++i) m = larger(m, lds[i]);
-  *most = m;
+  m = largest<16>(m, lds);
+  if (threadIdx.x == 0) *most = m;
 }
 
-// out[t] = x[t] scale[t] / *most; zeros for a token without a part in the gradients.
-__global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* x, int64_t ldx, const float* scale, const float* most,
-                                                   int64_t n, int H, uint16_t* out) {
-  const float m = *most;
+// out[t] = x[t] scale[t] / *most; zeros for a token without a part in the gradients.  Up to kFewTokens
+// tokens every workgroup finds the largest d_loss itself, which costs less than a launch before it.
+constexpr int kFewTokens = 2048;
+template <bool FEW>
+__global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* x, int64_t ldx, const float* d_loss,
+                                                   const int64_t* target, int64_t ignore, int V, int64_t rows,
+                                                   float* scale, float* most, int H, uint16_t* out) {
+  __shared__ float lds[4];
+  float m;
+  if (FEW) {
+    m = 0.0f;
+    for (int64_t t = threadIdx.x; t < rows; t += 256) {
+      const float a = scale_of(d_loss, target, ignore, V, t);
+      if (blockIdx.x == 0) scale[t] = a;
+      m = larger(m, a);
+    }
+    m = largest<4>(m, lds);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *most = m;
+  } else {
+    m = *most;
+  }
+  if (!out) return;
+  const int64_t n = rows * H;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 256 * 8) {
     const int64_t t = i / H;
-    const float a = scale[t], r = m != 0.0f ? a / m : a;
+    const float a = FEW ? scale_of(d_loss, target, ignore, V, t) : scale[t], r = m != 0.0f ? a / m : a;
     const u32x4_t q = *(const u32x4_t*)(x + t * ldx + (i - t * H));
     u32x4_t o;
 #pragma unroll
@@ -178,47 +246,57 @@ struct GradEpi {
 
   template <int RB0, int RB1, class ACC>
   __device__ __forceinline__ void tile(const TileArgs& p, const TileOut& o, ACC& acc, u32x4_t* lds) const {
-    float* st = (float*)lds + o.wave * (32 * ST_LD);
-    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) {
+    float* st = (float*)epi_stage(lds, o);
+    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) __attribute__((always_inline)) {
+      const int chunk = o.lane & 7, col = o.c0 + 64 * o.wn + 8 * chunk;
+      const bool whole = o.c0 + TB <= p.g.N;  // uniform
       float l[4], w[4];
-      int64_t t[4];
+      int64_t hit[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = row0 + i * 8 + (o.lane >> 3);
         const int64_t grow = o.p0 + (row < o.rows ? row : 0);
-        t[i] = target[grow];
-        l[i] = lse[grow];
+        hit[i] = target[grow] - v0 - col;
+        l[i] = -lse[grow] * LOG2E;
         w[i] = scale[grow];
       }
-      stage_block(st, ST_LD, o, a0, a1);
-      wave_sync();
-      const int at = (o.lane & 7) * 8, col = o.c0 + 64 * o.wn + at;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = i * 8 + (o.lane >> 3);
-        const f32x4_t* s = (const f32x4_t*)(st + row * ST_LD + at);
-        const f32x4_t x = s[0], y = s[1];
-        if (row0 + row >= o.rows || col >= p.g.N) continue;
-        const int64_t hit = t[i] - v0 - col;
-        float v[8];
+      for (int q = 0; q < 2; ++q) {
+        stage16(st, q, o.lane, a0, a1);
+        wave_sync();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float e = __expf((k < 4 ? x[k & 3] : y[k & 3]) - l[i]);
+        for (int j = 0; j < 2; ++j) {
+          const int i = 2 * q + j, row = j * 8 + (o.lane >> 3);
+          const f32x4_t x = *staged(st, row, 2 * chunk), y = *staged(st, row, 2 * chunk + 1);
+          if (row0 + 16 * q + row >= o.rows || col >= p.g.N) continue;
           // nothing for a token without a part, whatever its logits; columns past the vocabulary, which
           // the products read with the last eight, are zeros
-          v[k] = w[i] != 0.0f && col + k < p.g.N ? (hit == k ? e - 1.0f : e) : 0.0f;
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            v[k] = w[i] != 0.0f ? __builtin_amdgcn_exp2f(fmaf(k < 4 ? x[k & 3] : y[k & 3], LOG2E, l[i])) : 0.0f;
+          if (hit[i] >= 0 && hit[i] < 8 && w[i] != 0.0f)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] -= hit[i] == k ? 1.0f : 0.0f;
+          if (!whole)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = col + k < p.g.N ? v[k] : 0.0f;
+          *(u32x4_t*)(d + (o.p0 + row0 + 16 * q + row) * ldd + col) =
+              u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
         }
-        *(u32x4_t*)(d + (o.p0 + row0 + row) * ldd + col) = u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+        wave_sync();
       }
-      wave_sync();
     });
   }
 };
 
+template <bool CHAIN>
 __global__ __launch_bounds__(512, 1) void k_loss_grad(TileArgs p, GradEpi epi) {
   __shared__ u32x4_t lds[10 * HU];
-  row_tile<OP_NT, false, GX_ROWS>(p, lds, epi);
+  if constexpr (CHAIN)
+    row_chain<OP_NT>(p, lds, epi);
+  else
+    row_tile<OP_NT, false, GX_ROWS>(p, lds, epi);
 }
 
 // Adds a tile to what earlier pieces left (add = 0: the first piece).
@@ -229,9 +307,9 @@ struct SumEpi {
 
   template <int RB0, int RB1, class ACC>
   __device__ __forceinline__ void tile(const TileArgs& p, const TileOut& o, ACC& acc, u32x4_t* lds) const {
-    float* st = (float*)lds + o.wave * (32 * ST_LD);
-    const int at = (o.lane & 15) * 4, col = o.c0 + 128 * (at >> 5) + 32 * o.wn + (at & 31);
-    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) {
+    float* st = (float*)epi_stage(lds, o);
+    const int chunk = o.lane & 15, col = o.c0 + 128 * (chunk >> 3) + 32 * o.wn + 4 * (chunk & 7);
+    each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) __attribute__((always_inline)) {
       f32x4_t was[8];
       bool in[8];
 #pragma unroll
@@ -240,29 +318,57 @@ struct SumEpi {
         in[i] = row < o.rows && col < p.g.K;
         was[i] = in[i] && add ? *(const f32x4_t*)(out + (o.p0 + row) * p.g.K + col) : f32x4_t{0, 0, 0, 0};
       }
-      stage_block(st, ST_LD, o, a0, a1);
-      wave_sync();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = i * 4 + (o.lane >> 4);
-        const f32x4_t v = *(const f32x4_t*)(st + row * ST_LD + at);
-        if (in[i]) *(f32x4_t*)(out + (o.p0 + row0 + row) * p.g.K + col) = was[i] + v;
+      for (int q = 0; q < 2; ++q) {
+        stage16(st, q, o.lane, a0, a1);
+        wave_sync();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = 4 * q + j, row = j * 4 + (o.lane >> 4);
+          if (in[i]) *(f32x4_t*)(out + (o.p0 + row0 + 16 * q + row) * p.g.K + col) = was[i] + *staged(st, row, chunk);
+        }
+        wave_sync();
       }
-      wave_sync();
     });
   }
 };
 
-// One slice of a piece's reduction a workgroup row.
-__global__ __launch_bounds__(512, 1) void k_loss_dx(TileArgs p, SumEpi epi, int slice) {
+// Both products of a piece in one launch: the tiles of dw fill the compute units that dx's, which are
+// longer, leave.  dx: units (slice, row tile, panel) in eight equal runs, one for each XCD, whose L2 then
+// serves a slice's rows of d and w again.
+struct LossTiles {
+  TileArgs dx, dw;
+  SumEpi sum;
+  int dx_units;  // a multiple of 8
+  int slice, slices, row_tiles;
+};
+template <class EPI>
+__global__ __launch_bounds__(512, 1) void k_loss_products(LossTiles a) {
   __shared__ u32x4_t lds[10 * HU];
-  const int n0 = (int)blockIdx.y * slice;
-  if (n0 >= p.g.N) return;
+  const int b = blockIdx.x;
+  if (b >= a.dx_units) {
+    wgrad_tile<GX_ROWS, EPI>(a.dw, b - a.dx_units, lds);
+    return;
+  }
+  TileArgs p = a.dx;
+  const int per = a.row_tiles * p.npan, all = a.slices * per, run = a.dx_units / 8, unit = (b & 7) * run + (b >> 3);
+  if (unit >= all) return;
+  const int slice = unit / per, tile = unit - slice * per, n0 = slice * a.slice;
+  if (n0 >= p.g.N) return;  // the last piece has fewer
   p.a += (int64_t)n0 * 2;
   p.b += (int64_t)n0 * p.g.K * 2;
-  p.g.N = p.g.N - n0 < slice ? p.g.N - n0 : slice;
-  epi.out += (int64_t)blockIdx.y * p.g.rows * p.g.K;
-  row_tile<OP_NN, false, GX_ROWS>(p, lds, epi);
+  p.g.N = p.g.N - n0 < a.slice ? p.g.N - n0 : a.slice;
+  SumEpi sum = a.sum;
+  sum.out += (int64_t)slice * p.g.rows * p.g.K;
+  const int64_t p0 = (int64_t)(tile / p.npan) * TB;
+  const int rows = (int)(p.g.rows - p0 < TB ? p.g.rows - p0 : TB);
+  const TileJob job{0, p0, rows, 0, 0, tile % p.npan};
+  if (rows > 128)
+    tile_product<OP_NN, false, 2, 2, GX_ROWS, false, SumEpi>(p, job, lds, nullptr, sum);
+  else if (rows > 64)
+    tile_product<OP_NN, false, 2, 0, GX_ROWS, false, SumEpi>(p, job, lds, nullptr, sum);
+  else
+    tile_product<OP_NN, false, 1, 0, GX_ROWS, false, SumEpi>(p, job, lds, nullptr, sum);
 }
 
 // dx = the sum of its slices, times the token's d_loss.
@@ -291,6 +397,14 @@ __global__ __launch_bounds__(256) void k_loss_dx_sum(const float* part, int slic
   }
 }
 
+// One launch of row tiles of one group.
+template <class F, class EPI>
+hipError_t launch_rows(const Launch& lc, F chained, F single, const TileArgs& t, const EPI& epi) {
+  const int64_t units = row_tile_units(t.g, t.npan);
+  if (takes_chain(t.g, units)) return launch(lc, chained, dim3((unsigned)kChainGroups), dim3(512), t, epi);
+  return launch(lc, single, dim3((unsigned)units), dim3(512), t, epi);
+}
+
 Groups one_matrix(int64_t rows, int64_t ldx, int64_t ldy, int N, int K) {
   return Groups{rows, rows, ldx, ldy, 1, N, K, 1, nullptr, nullptr};
 }
@@ -314,8 +428,7 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s) {
   t.b = (const char*)a.w;
   t.npan = panels;
   const Launch lc{s, nullptr, nullptr};
-  hipError_t e = launch(lc, k_loss_logits, dim3((unsigned)row_tile_units(t.g, panels)), dim3(512), t,
-                        LseEpi{a.target, a.rows, part, hit});
+  hipError_t e = launch_rows(lc, k_loss_logits<true>, k_loss_logits<false>, t, LseEpi{a.target, a.rows, part, hit});
   if (e != hipSuccess) return e;
   const int64_t joins = (a.rows + JR - 1) / JR;
   return launch(lc, k_loss_join, dim3((unsigned)(joins < (1 << 20) ? joins : 1 << 20)), dim3(JR * 16), (const float2*)part,
@@ -337,10 +450,15 @@ LossPlan loss_plan(int64_t rows, int V, int H) {
   }
   p.slice = ((first + p.slices - 1) / p.slices + 63) / 64 * 64;
   p.slices = (first + p.slice - 1) / p.slice;  // none of the first piece's is empty
+  // parts of dw: as many as fit the 256 workgroups, of at least four steps of 64 tokens
+  const int64_t units = ((first + TB - 1) / TB) * (int64_t)((H + TB - 1) / TB), parts = kChainGroups / units;
+  p.splits = (int)(parts < rows / 256 ? parts : rows / 256);
+  if (p.splits < 1) p.splits = 1;
   p.d_bytes = align256((size_t)rows * p.piece * 2);
   p.part_bytes = align256((size_t)p.slices * rows * H * 4);
   p.x_bytes = align256((size_t)rows * H * 2);
-  p.bytes = p.d_bytes + p.part_bytes + p.x_bytes + align256((size_t)rows * 4) + 256;
+  p.dw_bytes = p.splits > 1 ? align256((size_t)p.splits * first * H * 4) : 0;
+  p.bytes = p.d_bytes + p.part_bytes + p.x_bytes + p.dw_bytes + align256((size_t)rows * 4) + 256;
   return p;
 }
 
@@ -349,16 +467,21 @@ hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
   uint16_t* d = (uint16_t*)workspace;
   float* part = (float*)((char*)workspace + plan.d_bytes);
   uint16_t* x = (uint16_t*)((char*)part + plan.part_bytes);
-  float* most = (float*)((char*)x + plan.x_bytes);
+  float* dw_part = (float*)((char*)x + plan.x_bytes);
+  float* most = (float*)((char*)dw_part + plan.dw_bytes);
   float* scale = most + 64;
   const Launch lc{s, nullptr, nullptr};
   const int64_t total = a.rows * a.H, groups = (total / 8 + 255) / 256;
-  const dim3 each((unsigned)(groups < 8192 ? groups : 8192));
+  const dim3 each((unsigned)(groups < 1024 ? groups : 1024));
   if (a.rows > 0) {
-    hipError_t e = launch(lc, k_loss_scale, dim3(1), dim3(1024), a.d_loss, a.target, a.ignore, a.V, a.rows, scale, most);
-    if (e == hipSuccess && a.dw)
-      e = launch(lc, k_loss_rows, each, dim3(256), (const uint16_t*)a.x, a.ldx, (const float*)scale, (const float*)most,
-                 total, a.H, x);
+    const bool few = a.rows <= kFewTokens;
+    hipError_t e = hipSuccess;
+    if (!few)
+      e = launch(lc, k_loss_scale, dim3(1), dim3(1024), a.d_loss, a.target, a.ignore, a.V, a.rows, scale, most);
+    if (e == hipSuccess && (few || a.dw))
+      e = launch(lc, few ? k_loss_rows<true> : k_loss_rows<false>, few && !a.dw ? dim3(1) : each, dim3(256),
+                 (const uint16_t*)a.x, a.ldx, a.d_loss, a.target, a.ignore, a.V, a.rows, scale, most, a.H,
+                 a.dw ? x : nullptr);
     if (e != hipSuccess) return e;
   }
   for (int64_t v0 = 0; v0 < a.V; v0 += plan.piece) {
@@ -371,25 +494,37 @@ hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
     t.npan = (n + TB - 1) / TB;
     hipError_t e = hipSuccess;
     if (a.rows > 0) {
-      e = launch(lc, k_loss_grad, dim3((unsigned)row_tile_units(t.g, t.npan)), dim3(512), t,
-                 GradEpi{a.target, (int)v0, a.lse, scale, d, (int64_t)plan.piece});
+      e = launch_rows(lc, k_loss_grad<true>, k_loss_grad<false>, t,
+                      GradEpi{a.target, (int)v0, a.lse, scale, d, (int64_t)plan.piece});
       if (e != hipSuccess) return e;
     }
-    if (a.dx && a.rows > 0) {
-      TileArgs u = t;
-      u.a = (const char*)d;
-      u.npan = (a.H + TB - 1) / TB;
-      e = launch(lc, k_loss_dx, dim3((unsigned)row_tile_units(u.g, u.npan), (unsigned)plan.slices), dim3(512), u,
-                 SumEpi{part, v0 > 0}, plan.slice);
-      if (e != hipSuccess) return e;
-    }
-    if (a.dw) {
-      Groups g = t.g;
-      g.ldx = a.H;
-      e = launch_op_tile(OP_TN, false, g, d, x, Scales{}, (char*)a.dw + v0 * a.H * (a.dw32 ? 4 : 2), a.dw32, s,
-                         a.rows > 0 ? most : nullptr);
-      if (e != hipSuccess) return e;
-    }
+    LossTiles f{};
+    f.dx = t;
+    f.dx.a = (const char*)d;
+    f.dx.npan = (a.H + TB - 1) / TB;
+    f.sum = SumEpi{part, v0 > 0};
+    f.slice = plan.slice;
+    f.slices = plan.slices;
+    f.row_tiles = (int)((a.rows + TB - 1) / TB);
+    if (a.dx) f.dx_units = (plan.slices * f.row_tiles * f.dx.npan + 7) / 8 * 8;
+    f.dw = t;
+    f.dw.g.ldx = a.H;
+    f.dw.a = (const char*)d;
+    f.dw.b = (const char*)x;
+    f.dw.nrow = (n + TB - 1) / TB;
+    f.dw.npan = f.dx.npan;
+    f.dw.splits = plan.splits;
+    f.dw.factor = most;
+    void* dw = a.dw ? (char*)a.dw + v0 * a.H * (a.dw32 ? 4 : 2) : nullptr;
+    f.dw.out = plan.splits > 1 ? dw_part : dw;
+    f.dw.fp32 = plan.splits > 1 || a.dw32;
+    const int64_t units = f.dx_units + (a.dw ? wgrad_units(f.dw.g, plan.splits) : 0);
+    // the factor comes with the sum of the parts, and where there are no tokens there is none
+    e = launch(lc, plan.splits > 1 || a.rows == 0 ? k_loss_products<StoreEpi> : k_loss_products<ScaledEpi>,
+               dim3((unsigned)units), dim3(512), f);
+    if (e == hipSuccess && a.dw && plan.splits > 1)
+      e = launch_sum_parts(dw_part, plan.splits, (int64_t)n * a.H, most, dw, a.dw32, s);
+    if (e != hipSuccess) return e;
   }
   if (!a.dx || a.rows == 0) return hipSuccess;
   return launch(lc, k_loss_dx_sum, each, dim3(256), (const float*)part, plan.slices, total, a.H, a.lddx,

@@ -26,7 +26,8 @@ struct TileArgs {
   int fp32;
   int npan;    // tiles along the second output dimension
   int nrow;    // TN: tiles along n
-  const float* factor;  // TN: the results are multiplied by it (NULL: not)
+  int splits;           // TN: parts of the reduction (0 and 1: the whole)
+  const float* factor;  // ScaledEpi
 };
 
 // Transfers go through range-checked buffer descriptors: a lane whose offset
@@ -94,6 +95,20 @@ __device__ __forceinline__ void bar() {
   asm volatile("" ::: "memory");
 }
 
+// The wave's LDS writes are visible to its own reads, and its reads done before its next writes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// v, unknown to the compiler: what follows from it is computed here, not carried from one tile to the
+// next in registers that the loop needs.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // The row tile and panel of a workgroup: group, first row, rows.  A group of c
 // rows has ceil(c / 256) tiles, all of 256 rows but the last.
 struct RowTile {
@@ -104,6 +119,9 @@ struct RowTile {
   int once;  // the group's only tile, of weight rows in whole cache lines
 };
 
+// Workgroups of a launch whose tiles follow each other: one a compute unit.
+constexpr int kChainGroups = 256;
+
 // One group: the units (tile, panel) are cut into eight equal runs, one for
 // each XCD, and within a run into blocks of four tiles, panel by panel: the 32
 // workgroups that an XCD runs at a time then read about as many tiles' rows as
@@ -111,12 +129,17 @@ struct RowTile {
 __device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int64_t local, int npan, bool aligned) {
   constexpr int SG = 4;
   const int64_t total = (g.rows + TB - 1) / TB;
+  // Where all units run at a time, the tiles share the rows evenly, in whole blocks of 32: the tallest one
+  // takes the time of the launch (257 rows against 32003 columns of 2048: 256 + 1 rows 56 us, 160 + 97 50).
+  const int height_rows = total * npan <= kChainGroups ? (int)((g.rows + 32 * total - 1) / (32 * total)) * 32 : TB;
   const int64_t run = (total * npan + 7) / 8, unit = xcd * run + local;
   if (local >= run || unit >= total * npan) return RowTile{-1, 0, 0, 0, 0};
   const int64_t sg = unit / (SG * npan), sr = unit - sg * SG * npan;
   const int64_t height = total - sg * SG < SG ? total - sg * SG : SG;
-  const int64_t p0 = (sg * SG + sr % height) * TB;
-  return RowTile{0, p0, (int)(g.rows - p0 < TB ? g.rows - p0 : TB), (int)(sr / height), total == 1 && aligned};
+  const int64_t p0 = (sg * SG + sr % height) * height_rows;
+  if (p0 >= g.rows) return RowTile{-1, 0, 0, 0, 0};
+  return RowTile{0, p0, (int)(g.rows - p0 < height_rows ? g.rows - p0 : height_rows), (int)(sr / height),
+                 total == 1 && aligned};
 }
 
 // Groups: the tiles in three classes, the tallest first, so that the short
@@ -242,8 +265,14 @@ enum { GX_ROWS = 0, GX_INDEX = 1, GX_FAR = 2 };
 // 128 columns of each: column half j holds those of matrix j, so that a wave has
 // the same 32 columns of both in the same registers.
 struct StoreEpi {
-  static constexpr bool kGated = false;
+  static constexpr bool kGated = false, kFactor = false;
 };
+// The same, times p.factor (a type of its own: the products cost short weight gradients 3%).
+struct ScaledEpi {
+  static constexpr bool kGated = false, kFactor = true;
+};
+template <class EPI>
+constexpr bool kStores = std::is_same<EPI, StoreEpi>::value || std::is_same<EPI, ScaledEpi>::value;
 // Where an epilogue's tile lies, and the thread's place in it.
 struct TileOut {
   int64_t p0;       // first row
@@ -251,10 +280,53 @@ struct TileOut {
   int c0, panel;    // first column, panel
   int tid, wave, wm, wn, lane;
 };
-template <OpKind KIND, bool I8, int RB0, int RB1, int GX, bool ONCE, class EPI = StoreEpi>
-__device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p0, int rows, int64_t len, int r0t,
-                                             int panel, u32x4_t* lds, int32_t* gidx, const EPI& epi = EPI{}) {
-  constexpr bool GATED = EPI::kGated;
+// A tile: expert, first row of its group's rows, rows of it that exist (NT, NN) or rows to reduce (TN),
+// tile along n (TN), panel.
+struct TileJob {
+  int e;
+  int64_t p0;
+  int rows;
+  int64_t len;
+  int r0t, panel;
+};
+// next(job): the workgroup's following tile, if it is of the same kind.  With one, its first transfers
+// are issued before the epilogue of the tile at hand, which then hides their way: a tile of 256 x 256
+// costs 9.5 us beside its steps without it (4096 x 16384 x 256 .. 4096, at 1.45 us a step).
+struct NoNext {
+  static constexpr bool kChain = false;
+  __device__ __forceinline__ bool operator()(TileJob&) const { return false; }
+};
+template <class F>
+struct ChainNext {
+  static constexpr bool kChain = true;
+  F f;
+  __device__ __forceinline__ bool operator()(TileJob& t) const { return f(t); }
+};
+template <class F>
+__device__ __forceinline__ ChainNext<F> chain_next(F f) {
+  return ChainNext<F>{f};
+}
+// Row tiles of one group do where there are more, and where few of their rows are missing ones: a short
+// tile alone costs less than a whole one (1 to 192 rows 0.4 to 0.8 of it).
+inline bool takes_chain(const Groups& g, int64_t units) {
+  const int64_t rest = g.rows % TB;
+  return !g.offsets && units > kChainGroups && (rest == 0 || rest > 192 || g.rows >= 8 * TB);
+}
+// LDS of the epilogues, a part of each wave's own: of tiles that follow each other the 32 KB behind the
+// stages of two whole row halves, else any 64 KB.
+constexpr int EPI_AT = 8 * HU;
+template <bool CHAIN>
+constexpr int kEpiUnits = CHAIN ? HU / 4 : HU / 2;
+template <bool CHAIN>
+__device__ __forceinline__ u32x4_t* epi_lds(u32x4_t* lds, int wave) {
+  return lds + (CHAIN ? EPI_AT : HU) + wave * kEpiUnits<CHAIN>;
+}
+
+template <OpKind KIND, bool I8, int RB0, int RB1, int GX, bool ONCE, class EPI = StoreEpi, class NEXT = NoNext>
+__device__ __forceinline__ void tile_product(const TileArgs& p, TileJob job, u32x4_t* lds, int32_t* gidx,
+                                             const EPI& epi = EPI{}, const NEXT& next = NEXT{}) {
+  constexpr bool GATED = EPI::kGated, CHAIN = NEXT::kChain;
+  static_assert(!CHAIN || (RB0 == 2 && RB1 == 2 && !I8), "tiles in a row are whole ones");
   static_assert(!GATED || (KIND == OP_NT && !I8), "two matrices an expert: bf16 NT products");
   constexpr bool AT = KIND == OP_TN, BT = KIND != OP_NT;  // operand reduces across its rows
   constexpr int ES = I8 ? 1 : 2;                          // bytes an element
@@ -276,7 +348,13 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   auto sa = [&](int h, int st) { return lds + st * STAGE + 2 * HU + (h ? RB0 * HU / 2 : 0); };
 
   const int ncols = KIND == OP_NT ? g.N : g.K;
-  const int c0 = panel * (GATED ? TB / 2 : TB);
+  // the tile whose steps run, or are being fetched
+  int e = 0, rows = 0, r0t = 0, c0 = 0;
+  int64_t p0 = 0, len = 0;
+  auto set_job = [&](const TileJob& t) __attribute__((always_inline)) {
+    e = t.e, p0 = t.p0, rows = t.rows, len = t.len, r0t = t.r0t;
+    c0 = t.panel * (GATED ? TB / 2 : TB);
+  };
   constexpr int BKE = I8 ? 128 : 64;  // reduction elements of a step
   // first column of the tile's 32-column block wn of column half j.  Weights read along memory: a
   // wave's two blocks side by side, so that it writes whole cache lines; across: halves of 128.
@@ -289,12 +367,11 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   // banks.  Across-rows operand: 4 stage rows of 256 bytes, lane -> row
   // lane/16, position lane%16, source chunk position ^ 4 (row % 4): the four
   // rows a transposing read takes together lie in different 64-byte parts.
-  const int lr = lane >> 3;
   constexpr bool G64 = GX == GX_FAR;
   const bool gather = KIND == OP_TN ? GX != GX_ROWS : KIND == OP_NT && g.perm;
   const int64_t lda = KIND == OP_NT ? g.ldx : g.ldy;
-  int64_t red = KIND == OP_NT ? g.K : KIND == OP_NN ? g.N : len;  // reduction length (TN: of this chunk)
-  int64_t base = p0;                                              // TN: first row of the chunk
+  int64_t red = KIND == OP_NT ? g.K : g.N;  // reduction length (TN: of this chunk)
+  int64_t base = 0;                         // TN: first row of the chunk
   int nsteps = 0, last = 0;  // steps; reduction elements of the last one
   // window of the first step, and what a step adds to its base (across) or to the offsets (along: 128)
   const char *abase, *bbase;
@@ -310,7 +387,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   uint32_t aoff[2][RBM], boff[2][2];  // a lane's offsets in its window
   bool aend[2][RBM], bend[2][2];      // along: the lane's chunk lies in the last step
   const char* a64[2][RBM];
-  auto set_steps = [&]() {
+  auto set_steps = [&]() __attribute__((always_inline)) {
     nsteps = (int)((red + BKE - 1) / BKE);
     last = (int)(red - (int64_t)(nsteps - 1) * BKE);
     if (AT) {
@@ -330,7 +407,8 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       bbytes = ((g.x_rows - 1) * g.ldx + g.K) * 2;  // gathered
     }
   };
-  auto set_a = [&]() {
+  auto set_a = [&]() __attribute__((always_inline)) {
+    const int lane = CHAIN ? here(tid & 63) : tid & 63, lr = lane >> 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -356,7 +434,8 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
         }
       }
   };
-  auto set_b = [&]() {
+  auto set_b = [&]() __attribute__((always_inline)) {
+    const int lane = CHAIN ? here(tid & 63) : tid & 63, lr = lane >> 3;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -375,7 +454,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
         }
       }
   };
-  auto load_a = [&](int h, int st, int s) {
+  auto load_a = [&](int h, int st, int s) __attribute__((always_inline)) {
     const int sc = s < nsteps ? s : nsteps - 1;
 #pragma unroll
     for (int i = 0; i < RBM; ++i) {
@@ -391,7 +470,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     }
   };
   const int64_t bhalf = GATED ? (int64_t)g.N * g.K * 2 : 0;  // from an expert's first matrix to its second
-  auto load_b = [&](int j, int st, int s) {
+  auto load_b = [&](int j, int st, int s) __attribute__((always_inline)) {
     const int sc = s < nsteps ? s : nsteps - 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -419,12 +498,6 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
   };
 
   acc_t acc[2][RBM][2];  // [row half][block][column half]
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int b = 0; b < RBM; ++b)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[h][b][j] = (acc_t){};
 
   // ---- operand reads: sub-step kk, lane half take the reduction elements
   // 32 half + 8 kk .. +8 of a step (int8: 64 half + 16 kk .. +16) on both operands
@@ -444,7 +517,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     return u32x4_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
   };
   u32x4_t af[RBM][4], bf[2][4];
-  auto read_a = [&](int h, int st) {
+  auto read_a = [&](int h, int st) __attribute__((always_inline)) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -454,13 +527,13 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
         af[b][kk] = AT ? read_across(sa(h, st), r, kk) : read_along(sa(h, st), r, kk);
       }
   };
-  auto read_b = [&](int j, int st) {
+  auto read_b = [&](int j, int st) __attribute__((always_inline)) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
       bf[j][kk] = BT ? read_across(sb(j, st), 32 * wn, kk) : read_along(sb(j, st), 32 * wn, kk);
   };
   // the multiply part of a cluster, between its two barriers
-  auto multiply = [&](int h, int j) {
+  auto multiply = [&](int h, int j) __attribute__((always_inline)) {
     bar();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
@@ -483,24 +556,103 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
     bar();
   };
 
-  // One pass over the reduction; weight gradients with gathered rows pass in
-  // chunks whose row indexes fit the LDS.
-  for (int64_t done = 0; KIND != OP_TN ? done == 0 : done < len; done += GI) {
-    if (KIND == OP_TN && gather) {
-      red = len - done < GI ? len - done : GI;
+  // ---- epilogue.  Block layout: lane -> column lane%32, register r -> row
+  // 8 (r/4) + 4 (lane/32) + r%4.
+  auto epilogue_of = [&](const TileOut& at, int c0, int rows, int e, int r0t, int64_t p0) __attribute__((always_inline)) {
+    const int lane = at.lane, half = lane >> 5, l32 = lane & 31;
+    if constexpr (!kStores<EPI>) {
+      epi.template tile<RB0, RB1>(p, at, acc, lds);
+      return;
+    } else {
+    const int nrows = KIND == OP_TN ? (g.N - r0t * TB < TB ? g.N - r0t * TB : TB) : rows;
+    const int64_t ldo = KIND == OP_NT ? g.ldy : KIND == OP_NN ? g.ldx : g.K;
+    const int64_t row_base = KIND == OP_TN ? (int64_t)e * g.N + (int64_t)r0t * TB : p0;
+    float* s_scale = (float*)lds;  // I8: the rows' scales
+    if (I8) {
+      if (tid < rows) {
+        const int64_t t = source_row(g, p0 + tid);
+        s_scale[tid] = t < 0 ? 0.0f : p.sc.x[t];
+      }
+      __syncthreads();
+    }
+    float ws[2] = {1.0f, 1.0f}, bi[2] = {0.0f, 0.0f};
+    if (I8) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = c0 + col_of(j, wn) + l32;
+        if (n < ncols) {
+          ws[j] = p.sc.w[(int64_t)e * g.N + n];
+          if (p.sc.bias) bi[j] = p.sc.bias[n];
+        }
+      }
+    }
+    float factor = 1.0f;
+    if constexpr (EPI::kFactor) factor = *p.factor;
+    // 64 columns of some of a block's rows at a time through a part of the LDS of the wave's own, then
+    // 16 bytes a lane
+    auto write = [&](auto type) __attribute__((always_inline)) {
+      typedef decltype(type) T;
+      constexpr int EC = 16 / sizeof(T);                            // results of a 16-byte chunk
+      constexpr int RT = kEpiUnits<CHAIN> * 16 / (64 * sizeof(T)), PR = RT < 32 ? RT : 32;  // rows at a time
+      T* st = (T*)epi_lds<CHAIN>(lds, wave);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < RBM; ++b) {
+          if (b >= (h ? RB1 : RB0)) continue;
+          const int row0 = (h ? 64 * RB0 : 0) + 32 * ((h ? RB1 : RB0) * wm + b);
+#pragma unroll
+          for (int q = 0; q < 32 / PR; ++q) {
+            if (row0 + PR * q >= nrows) continue;  // uniform
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int r = PR / 2 * q; r < PR / 2 * (q + 1); ++r) {
+                const int row = 8 * (r >> 2) + 4 * half + (r & 3);
+                float v;
+                if constexpr (I8)
+                  v = (float)acc[h][b][j][r] * (s_scale[row0 + row] * ws[j]) + bi[j];
+                else
+                  v = EPI::kFactor ? acc[h][b][j][r] * factor : acc[h][b][j][r];
+                if constexpr (sizeof(T) == 4)
+                  st[(row - PR * q) * 64 + 32 * j + l32] = v;
+                else
+                  st[(row - PR * q) * 64 + 32 * j + l32] = (T)f32_to_bf16(v);
+              }
+            wave_sync();
+#pragma unroll
+            for (int i = 0; i < PR / EC; ++i) {
+              const int c = i * 64 + lane;
+              const int row = c / (64 / EC), at = c % (64 / EC) * EC;  // column among the wave's 64
+              const int grow = row0 + PR * q + row, col = c0 + col_of(at >> 5, wn) + (at & 31);
+              if (grow < nrows && col < ncols)
+                *(u32x4_t*)((T*)p.out + (row_base + grow) * ldo + col) = *(const u32x4_t*)(st + row * 64 + at);
+            }
+            wave_sync();
+          }
+        }
+    };
+    if (p.fp32)
+      write(0.0f);
+    else
+      write((uint16_t)0);
+    }
+  };
+
+  // The first transfers of a pass over the reduction from its row `done` on.
+  auto prologue = [&](int64_t done) __attribute__((always_inline)) {
+    if (KIND == OP_TN) {
+      red = gather && len - done > GI ? GI : len - done;
       base = p0 + done;
+    }
+    if (KIND == OP_TN && gather) {
       // up to a whole number of steps, rows past the end as -1
       for (int i = tid; i < (red + 63) / 64 * 64; i += 512) gidx[i] = i < red ? (int32_t)source_row(g, base + i) : -1;
       __syncthreads();
-    } else if (done > 0) {
-      break;
     }
     set_steps();
     set_b();
     if constexpr (RB1 > 0) {
-      // memory parts: 8, 4, 8 and 4 reads of a block, two transfers a wave in each.  The first column
-      // half of a step is read in the last part of the step before.
-      constexpr int WB = 6 + RB0 + 2 * RB1, WA = 6 + 2 * RB0 + RB1;
       // the columns' transfers are on their way while the rows' indexes are read
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
@@ -513,45 +665,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
         load_a(0, d, d);
         load_a(1, d, d);
       }
-      wait_vm<RB0 + 2 * RB1>();  // all columns, first row half of step 0
-      bar();
-      read_b(0, 0);
-      // read by every wave before the first memory part refills it
-      wait_vm<63>();
-      bar();
-      if (wm == 1) bar();
-      for (int s0 = 0; s0 < nsteps; s0 += 2) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int s = s0 + u;
-          if (s >= nsteps) break;  // uniform
-          read_a(0, u);
-          load_b(0, u, s + 2);
-          wait_vm<WB>();  // second column half of this step
-          multiply(0, 0);
-          read_b(1, u);
-          load_a(0, u, s + 2);
-          // second row half of this step; in step 0 fewer transfers come after it than later on
-          if (s == 0)
-            wait_vm<2 + 2 * RB0 + RB1>();
-          else
-            wait_vm<WA>();
-          multiply(0, 1);
-          read_a(1, u);
-          load_b(1, u, s + 2);
-          wait_vm<WA>();  // first column half of the next step
-          multiply(1, 0);
-          read_b(0, u ^ 1);
-          load_a(1, u, s + 2);
-          if (s == 0)  // first row half of the next step
-            wait_vm<4 + RB0 + 2 * RB1>();
-          else
-            wait_vm<WB>();
-          multiply(1, 1);
-        }
-      }
     } else {
-      constexpr int W = 2 * (ST - 1) + (ST - 2) * (RB0 + 2);
 #pragma unroll
       for (int d = 0; d < ST; ++d) {
         load_b(0, d, d);
@@ -560,120 +674,125 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, int e, int64_t p
       set_a();
 #pragma unroll
       for (int d = 0; d < ST; ++d) load_a(0, d, d);
-      wait_vm<(ST - 1) * RB0>();  // all columns, rows of step 0
-      bar();
-      read_b(0, 0);
-      if (wm == 1) bar();
-      for (int s0 = 0; s0 < nsteps; s0 += ST) {
-#pragma unroll
-        for (int u = 0; u < ST; ++u) {
-          const int s = s0 + u;
-          if (s >= nsteps) break;  // uniform
-          read_a(0, u);
-          load_b(1, (u + ST - 1) % ST, s + ST - 1);
-          // second column half of this step, first halves of the next; in the first steps fewer
-          // transfers come after those than later on
-          if (s == 0)
-            wait_vm<(ST - 2) * RB0 + 2>();
-          else if (ST == 4 && s == 1)
-            wait_vm<(ST - 2) * RB0 + 6>();
-          else
-            wait_vm<W>();
-          multiply(0, 0);
-          read_b(1, u);
-          read_b(0, (u + 1) % ST);
-          load_a(0, u, s + ST);
-          load_b(0, u, s + ST);
-          wait_vm<63>();
-          multiply(0, 1);
-        }
-      }
     }
-    if (wm == 0) bar();
-    // transfers of steps past the end have landed and every wave has read its
-    // last operands before the LDS is used again
-    wait_vm<0>();
-    bar();
-  }
+  };
 
-  // ---- epilogue.  Block layout: lane -> column lane%32, register r -> row
-  // 8 (r/4) + 4 (lane/32) + r%4.
-  if constexpr (!std::is_same<EPI, StoreEpi>::value) {
-    epi.template tile<RB0, RB1>(p, TileOut{p0, rows, c0, panel, tid, wave, wm, wn, lane}, acc, lds);
-    return;
-  }
-  const int nrows = KIND == OP_TN ? (g.N - r0t * TB < TB ? g.N - r0t * TB : TB) : rows;
-  const int64_t ldo = KIND == OP_NT ? g.ldy : KIND == OP_NN ? g.ldx : g.K;
-  const int64_t row_base = KIND == OP_TN ? (int64_t)e * g.N + (int64_t)r0t * TB : p0;
-  float* s_scale = (float*)lds;  // I8: the rows' scales
-  if (I8) {
-    if (tid < rows) {
-      const int64_t t = source_row(g, p0 + tid);
-      s_scale[tid] = t < 0 ? 0.0f : p.sc.x[t];
-    }
-    __syncthreads();
-  }
-  float ws[2] = {1.0f, 1.0f}, bi[2] = {0.0f, 0.0f};
-  if (I8) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = c0 + col_of(j, wn) + l32;
-      if (n < ncols) {
-        ws[j] = p.sc.w[(int64_t)e * g.N + n];
-        if (p.sc.bias) bi[j] = p.sc.bias[n];
-      }
-    }
-  }
-  const float factor = KIND == OP_TN && p.factor ? *p.factor : 1.0f;
-  // 32 x 64 results at a time through a part of the LDS of the wave's own, then 16 bytes a lane
-  float* stage = (float*)(lds + HU) + wave * (32 * 64);
-  auto write = [&](auto type) {
-    typedef decltype(type) T;
-    constexpr int EC = 16 / sizeof(T);  // results of a 16-byte chunk
-    T* st = (T*)stage;
+  bool fetched = false;  // the first transfers are on their way
+  set_job(job);
+  for (;;) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int b = 0; b < RBM; ++b) {
-        if (b >= (h ? RB1 : RB0)) continue;
-        const int row0 = (h ? 64 * RB0 : 0) + 32 * ((h ? RB1 : RB0) * wm + b);
-        if (row0 >= nrows) continue;  // uniform
+      for (int b = 0; b < RBM; ++b)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) acc[h][b][j] = (acc_t){};
+    // One pass over the reduction; weight gradients with gathered rows pass in
+    // chunks whose row indexes fit the LDS.
+    for (int64_t done = 0; KIND != OP_TN ? done == 0 : done < len; done += KIND != OP_TN ? 1 : gather ? GI : len) {
+      if (!fetched) prologue(done);
+      fetched = false;
+      if constexpr (RB1 > 0) {
+        // memory parts: 8, 4, 8 and 4 reads of a block, two transfers a wave in each.  The first column
+        // half of a step is read in the last part of the step before.  (Stores of the tile before count
+        // as transfers in these waits, which they only make longer.)
+        constexpr int WB = 6 + RB0 + 2 * RB1, WA = 6 + 2 * RB0 + RB1;
+        wait_vm<RB0 + 2 * RB1>();  // all columns, first row half of step 0
+        bar();
+        read_b(0, 0);
+        // read by every wave before the first memory part refills it
+        wait_vm<63>();
+        bar();
+        if (wm == 1) bar();
+        for (int s0 = 0; s0 < nsteps; s0 += 2) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int row = 8 * (r >> 2) + 4 * half + (r & 3);
-            float v;
-            if constexpr (I8)
-              v = (float)acc[h][b][j][r] * (s_scale[row0 + row] * ws[j]) + bi[j];
+          for (int u = 0; u < 2; ++u) {
+            const int s = s0 + u;
+            if (s >= nsteps) break;  // uniform
+            read_a(0, u);
+            load_b(0, u, s + 2);
+            wait_vm<WB>();  // second column half of this step
+            multiply(0, 0);
+            read_b(1, u);
+            load_a(0, u, s + 2);
+            // second row half of this step; in step 0 fewer transfers come after it than later on
+            if (s == 0)
+              wait_vm<2 + 2 * RB0 + RB1>();
             else
-              v = KIND == OP_TN ? acc[h][b][j][r] * factor : acc[h][b][j][r];
-            if constexpr (sizeof(T) == 4)
-              st[row * 64 + 32 * j + l32] = v;
+              wait_vm<WA>();
+            multiply(0, 1);
+            read_a(1, u);
+            load_b(1, u, s + 2);
+            wait_vm<WA>();  // first column half of the next step
+            multiply(1, 0);
+            read_b(0, u ^ 1);
+            load_a(1, u, s + 2);
+            if (s == 0)  // first row half of the next step
+              wait_vm<4 + RB0 + 2 * RB1>();
             else
-              st[row * 64 + 32 * j + l32] = (T)f32_to_bf16(v);
+              wait_vm<WB>();
+            multiply(1, 1);
           }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-        for (int c = lane; c < 32 * 64 / EC; c += 64) {
-          const int row = c / (64 / EC), at = c % (64 / EC) * EC;  // column among the wave's 64
-          const int grow = row0 + row, col = c0 + col_of(at >> 5, wn) + (at & 31);
-          if (grow < nrows && col < ncols)
-            *(u32x4_t*)((T*)p.out + (row_base + grow) * ldo + col) = *(const u32x4_t*)(st + row * 64 + at);
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      } else {
+        constexpr int W = 2 * (ST - 1) + (ST - 2) * (RB0 + 2);
+        wait_vm<(ST - 1) * RB0>();  // all columns, rows of step 0
+        bar();
+        read_b(0, 0);
+        if (wm == 1) bar();
+        for (int s0 = 0; s0 < nsteps; s0 += ST) {
+#pragma unroll
+          for (int u = 0; u < ST; ++u) {
+            const int s = s0 + u;
+            if (s >= nsteps) break;  // uniform
+            read_a(0, u);
+            load_b(1, (u + ST - 1) % ST, s + ST - 1);
+            // second column half of this step, first halves of the next; in the first steps fewer
+            // transfers come after those than later on
+            if (s == 0)
+              wait_vm<(ST - 2) * RB0 + 2>();
+            else if (ST == 4 && s == 1)
+              wait_vm<(ST - 2) * RB0 + 6>();
+            else
+              wait_vm<W>();
+            multiply(0, 0);
+            read_b(1, u);
+            read_b(0, (u + 1) % ST);
+            load_a(0, u, s + ST);
+            load_b(0, u, s + ST);
+            wait_vm<63>();
+            multiply(0, 1);
+          }
+        }
       }
-  };
-  if (p.fp32)
-    write(0.0f);
-  else
-    write((uint16_t)0);
-}
+      if (wm == 0) bar();
+      // transfers of steps past the end have landed and every wave has read its
+      // last operands before the LDS is used again
+      wait_vm<0>();
+      bar();
+    }
 
+    const int c0t = c0, rowst = rows, et = e, r0tt = r0t;  // of the tile that is done
+    const int64_t p0t = p0;
+    const int ln = CHAIN ? here(lane) : lane;
+    const TileOut at{p0, rows, c0, job.panel, wave * 64 + ln, wave, wm, wn, ln};
+    bool more = false;
+    if constexpr (CHAIN) {
+      more = next(job);
+      if (more) {
+        set_job(job);
+        if (KIND != OP_TN || len > 0) {
+          prologue(0);
+          fetched = true;
+        }
+      }
+    }
+    epilogue_of(at, c0t, rowst, et, r0tt, p0t);
+    if (!CHAIN || !more) break;
+    // the epilogue's LDS is free again for every wave
+    wait_vm<63>();
+    bar();
+  }
+}
 // The workgroup's tile of a row-tiled product (NT, NN).  Workgroup b runs on XCD
 // b % 8; a row tile's panels stay on one XCD, whose L2 then serves the tile's
 // rows again.
@@ -684,8 +803,8 @@ __device__ __forceinline__ void row_tile(const TileArgs& p, u32x4_t* lds, const 
   tl = RowTile{__builtin_amdgcn_readfirstlane(tl.e), uniform64(tl.p0), __builtin_amdgcn_readfirstlane(tl.rows),
                __builtin_amdgcn_readfirstlane(tl.panel), __builtin_amdgcn_readfirstlane(tl.once)};
   if (tl.e < 0) return;
-  auto run = [&](auto r0, auto r1, auto once) {
-    tile_product<KIND, I8, r0(), r1(), GX, once(), EPI>(p, tl.e, tl.p0, tl.rows, 0, 0, tl.panel, lds, nullptr, epi);
+  auto run = [&](auto r0, auto r1, auto once) __attribute__((always_inline)) {
+    tile_product<KIND, I8, r0(), r1(), GX, once(), EPI>(p, TileJob{tl.e, tl.p0, tl.rows, 0, 0, tl.panel}, lds, nullptr, epi);
   };
   constexpr std::integral_constant<int, 0> c0{};
   constexpr std::integral_constant<int, 1> c1{};
@@ -709,6 +828,58 @@ __device__ __forceinline__ void row_tile(const TileArgs& p, u32x4_t* lds, const 
   }
 }
 
+// The same for one group of many tiles, in a launch of kChainGroups workgroups:
+// each takes every 32nd tile of its XCD, one after the other, and all of them as
+// whole ones.
+template <OpKind KIND, class EPI = StoreEpi>
+__device__ __forceinline__ void row_chain(const TileArgs& p, u32x4_t* lds, const EPI& epi = EPI{}) {
+  int64_t local = blockIdx.x >> 3;
+  auto take = [&](TileJob* t) __attribute__((always_inline)) {
+    const RowTile tl = find_tile_dense(p.g, blockIdx.x & 7, local, p.npan, false);
+    *t = TileJob{0, tl.p0, tl.rows, 0, 0, tl.panel};
+    return tl.e >= 0;
+  };
+  TileJob t;
+  if (!take(&t)) return;
+  tile_product<KIND, false, 2, 2, GX_ROWS, false, EPI>(p, t, lds, nullptr, epi,
+                                                       chain_next([&](TileJob& t) __attribute__((always_inline)) {
+                                                         local += kChainGroups / 8;
+                                                         return take(&t);
+                                                       }));
+}
+
+// Weight gradients: a unit is an expert, a part of its rows and a 256 x 256 tile
+// of its dw, in eight equal runs, one for each XCD: an expert's tiles share dy and
+// x in one L2.  Unit b of an XCD b % 8; returns the part, -1 past the end.
+inline int64_t wgrad_units(const Groups& g, int splits) {
+  return ((int64_t)g.E * splits * ((g.N + TB - 1) / TB) * ((g.K + TB - 1) / TB) + 7) / 8 * 8;
+}
+__device__ __forceinline__ int wgrad_unit(const TileArgs& p, int b, TileJob* t) {
+  const int parts = p.splits > 1 ? p.splits : 1, per = p.nrow * p.npan, all = p.g.E * parts * per;
+  const int run = (all + 7) / 8, local = b >> 3, unit = (b & 7) * run + local;
+  if (local >= run || unit >= all) return -1;
+  const int group = unit / per, tile = unit - group * per, e = group / parts, part = group - e * parts;
+  Range r = group_range(p.g, e);
+  if (parts > 1) {
+    // whole steps of rows each
+    const int64_t each = (r.size() + 64 * parts - 1) / (64 * parts) * 64, lo = r.lo + part * each;
+    r = Range{lo < r.hi ? lo : r.hi, lo + each < r.hi ? lo + each : r.hi};
+  }
+  *t = TileJob{e, uniform64(r.lo), 0, uniform64(r.size()), tile / p.npan, tile % p.npan};
+  return part;
+}
+// The tile of unit b; parts of a reduction as fp32, one after the other [part][E][N][K].
+template <int GX, class EPI = StoreEpi>
+__device__ __forceinline__ void wgrad_tile(const TileArgs& args, int b, u32x4_t* lds) {
+  static_assert(GI * 4 <= 2 * HU * 16, "indexes behind the stages");
+  TileJob t;
+  TileArgs p = args;
+  const int part = wgrad_unit(p, b, &t);
+  if (part < 0) return;
+  p.out = (char*)p.out + (int64_t)part * p.g.E * p.g.N * p.g.K * 4;
+  tile_product<OP_TN, false, 2, 2, GX, false, EPI>(p, t, lds, (int32_t*)(lds + 8 * HU));
+}
+
 // Workgroups of a launch of row tiles with npan panels each.
 inline int64_t row_tile_units(const Groups& g, int64_t npan) {
   const int64_t tiles = (g.rows + TB - 1) / TB + (g.offsets ? (g.E < g.rows ? g.E : g.rows) : 0);
@@ -724,12 +895,6 @@ inline bool rows_far(const Groups& g, int es) {
 
 // ---- for epilogues
 
-// The wave's LDS writes are visible to its own reads, and its reads done before its next writes.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
 // f(row0, a0, a1) for each 32-row block of the wave that has rows: its first row in the tile and the
 // accumulators of the two column halves.
 template <int RB0, int RB1, class ACC, class F>
@@ -746,6 +911,23 @@ __device__ __forceinline__ void each_block(const TileOut& o, ACC& acc, F&& f) {
 }
 // Row of a block that register r of a lane holds.
 __device__ __forceinline__ int block_row(int r, int lane) { return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); }
+// 4 KB of LDS of the wave, whether or not the tile has a follower.
+__device__ __forceinline__ void* epi_stage(u32x4_t* lds, const TileOut& o) { return epi_lds<true>(lds, o.wave); }
+// Rows 16 q .. +16 of a block there, columns 0..31 of the first column half, 32..63 of the second; the
+// 16-byte chunks of a row change places with its number, so that a chunk of all rows lies on all banks.
+__device__ __forceinline__ void stage16(float* st, int q, int lane, const f32x16_t& a0, const f32x16_t& a1) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = block_row(i, lane), col = lane & 31;
+    float* at = st + row * 64 + (((col >> 2) ^ row) & 15) * 4 + (col & 3);
+    *at = a0[8 * q + i];
+    at = st + row * 64 + (((col >> 2 | 8) ^ row) & 15) * 4 + (col & 3);
+    *at = a1[8 * q + i];
+  }
+}
+__device__ __forceinline__ const f32x4_t* staged(const float* st, int row, int chunk) {
+  return (const f32x4_t*)(st + row * 64 + ((chunk ^ row) & 15) * 4);
+}
 
 }  // namespace
 }  // namespace moe

@@ -26,6 +26,35 @@ Region mat_region(const moe_mat_t& m, int64_t rows, int64_t cols, moe_dtype_t t)
 }
 moe_status_t status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : hip_fail(e); }
 
+// A feed-forward block on checked shapes, and its workspace.
+struct Ffn {
+  FfnArgs a;
+  size_t d_pre_bytes, h_bytes, bytes;
+};
+moe_status_t check_ffn(const moe_feed_forward_t* d, Ffn* f) {
+  if (!d) return MOE_ERR_INVALID_ARG;
+  const moe_groups_t gu{d->rows, d->x_rows, d->ldx, 2 * (int64_t)std::max(d->I, 0), d->E, 2 * std::min(d->I, kMaxN), d->K,
+                        d->top_k, d->offsets, d->perm};
+  const moe_groups_t down{d->rows, d->rows, std::max<int64_t>(d->I, 0), d->ld_dy, d->E, d->H, d->I, 1, d->offsets, nullptr};
+  Checked c, e;
+  moe_status_t st = check_groups(&gu, 8, 8, &c);
+  if (st == MOE_OK) st = check_groups(&down, 8, 8, &e);
+  if (st == MOE_OK) st = check_x_rows(&gu);
+  if (st != MOE_OK) return st;
+  *f = Ffn{};
+  f->a.g = c.g;
+  f->a.I = d->I;
+  f->a.H = d->H;
+  f->a.ld_dy = d->ld_dy;
+  f->a.ld_dpre = 2 * (int64_t)d->I;
+  f->a.ld_h = d->I;
+  if (op_tile_units(OP_NN, e.g) > kOpMaxUnits || ffn_units(f->a) > kOpMaxUnits) return MOE_ERR_UNSUPPORTED_SHAPE;
+  f->d_pre_bytes = ((size_t)d->rows * 2 * d->I * 2 + 255) & ~(size_t)255;
+  f->h_bytes = ((size_t)d->rows * d->I * 2 + 255) & ~(size_t)255;
+  f->bytes = f->d_pre_bytes + f->h_bytes + ffn_split_bytes(f->a);
+  return MOE_OK;
+}
+
 moe_status_t check_combine(const moe_combine_t* d) {
   if (!d || d->tokens < 0 || d->rows < 0) return MOE_ERR_INVALID_ARG;
   if (d->H < 8 || d->H > kMaxK || d->H % 8 || d->top_k < 1 || d->top_k > kMaxTopK) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -160,7 +189,7 @@ moe_status_t check_loss(const moe_loss_t* d) {
   if (d->ldx > kMaxLd) return MOE_ERR_UNSUPPORTED_SHAPE;
   // tiles of the logits and of dx
   const int64_t rows = (d->rows + kOpTile - 1) / kOpTile, cols = std::max(d->V, d->H) / kOpTile + 1;
-  return rows * cols > kOpMaxUnits - 8 ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+  return rows * cols > kOpMaxUnits / 2 ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
 }
 LossArgs loss_args(const moe_loss_t* d, const void* x, const void* w, const int64_t* target) {
   LossArgs a{};
@@ -230,6 +259,64 @@ moe_status_t moe_gated_matmul_grad(const moe_groups_t* d, const void* dy, const 
   if (!r.disjoint()) return MOE_ERR_INVALID_ARG;
   return status_of(launch_gated_grad(c.g, dy, w, gate_up.data, gate_up.ld, d_gate_up.data, d_gate_up.ld, h, d->ldx,
                                      stream));
+}
+
+size_t moe_feed_forward_grad_workspace_size(const moe_feed_forward_t* d) {
+  Ffn f;
+  return check_ffn(d, &f) == MOE_OK ? f.bytes : 0;
+}
+
+moe_status_t moe_feed_forward_grad(const moe_feed_forward_t* d, const void* dy, const void* x, const void* w_gate_up,
+                                   const void* w_down, moe_mat_t gate_up, moe_mat_t dx, void* dw_gate_up, void* dw_down,
+                                   moe_dtype_t dw_type, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  Ffn f;
+  moe_status_t st = check_ffn(d, &f);
+  if (st != MOE_OK) return st;
+  if (!check_type(dw_type)) return MOE_ERR_INVALID_ARG;
+  if (!w_gate_up || !w_down || !dw_gate_up || !dw_down) return MOE_ERR_INVALID_ARG;
+  if (d->rows > 0 && (!dy || !gate_up.data || !dx.data || !workspace || (!x && d->x_rows > 0))) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({dy, x, w_gate_up, w_down, dw_gate_up, dw_down}) || !aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
+  const int64_t cols = 2 * (int64_t)d->I;
+  if (d->rows > 0 && ((st = check_mat(gate_up, cols)) != MOE_OK || (st = check_mat(dx, d->K)) != MOE_OK)) return st;
+  if (dx.ld > kMaxLd) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (d->rows > 0 && workspace_bytes < f.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t gu = (size_t)d->E * cols * d->K, down = (size_t)d->E * d->H * d->I;
+  Regions r;
+  r.input(matrix_at(dy, d->rows, d->ld_dy, d->H, 2));
+  r.input(matrix_at(x, d->x_rows, d->ldx, d->K, 2));
+  r.input(w_gate_up, gu * 2);
+  r.input(w_down, down * 2);
+  r.input(mat_region(gate_up, d->rows, cols, MOE_DT_BF16));
+  group_regions(&r, f.a.g);
+  r.output(mat_region(dx, d->rows, d->K, MOE_DT_BF16));
+  r.output(dw_gate_up, gu * type_size(dw_type));
+  r.output(dw_down, down * type_size(dw_type));
+  r.output(workspace, d->rows > 0 ? f.bytes : 0);
+  if (!r.disjoint()) return MOE_ERR_INVALID_ARG;
+  // workspace: d_pre, h, parts of the weight gradients
+  char* const d_pre = (char*)workspace;
+  char* const h = d_pre + f.d_pre_bytes;
+  if (d->rows > 0) {
+    Groups g = f.a.g;  // of the down projection
+    g.N = d->H;
+    g.K = d->I;
+    g.ldy = d->ld_dy;
+    g.perm = nullptr;
+    st = status_of(launch_gated_grad(g, dy, w_down, gate_up.data, gate_up.ld, d_pre, cols, h, d->I, stream));
+    if (st != MOE_OK) return st;
+  }
+  FfnArgs a = f.a;
+  a.dy = dy;
+  a.x = x;
+  a.w_gate_up = w_gate_up;
+  a.d_pre = d_pre;
+  a.h = h;
+  a.dx = dx.data;
+  a.ld_dx = dx.ld;
+  a.dw_gate_up = dw_gate_up;
+  a.dw_down = dw_down;
+  a.dw32 = dw_type == MOE_DT_FP32;
+  return status_of(launch_ffn_products(a, (float*)(h + f.h_bytes), stream));
 }
 
 moe_status_t moe_invert_permutation(int64_t rows, const int32_t* perm, const int32_t* offsets, int32_t E, int64_t n,

@@ -37,7 +37,8 @@ except ImportError as e:  # not built, or built against another torch
 EXPORTS = ("moe_grouped_matmul", "moe_grouped_matmul_grad_input", "moe_grouped_matmul_grad_weight",
            "moe_quantize_i8", "moe_matmul_i8_workspace_size", "moe_matmul_i8", "moe_block_norm",
            "moe_block_norm_grad", "moe_block_merge", "moe_block_merge_grad", "moe_norm_grad_workspace_size",
-           "moe_gated_matmul", "moe_gated_matmul_grad", "moe_invert_permutation", "moe_combine", "moe_combine_grad",
+           "moe_gated_matmul", "moe_gated_matmul_grad", "moe_feed_forward_grad_workspace_size",
+           "moe_feed_forward_grad", "moe_invert_permutation", "moe_combine", "moe_combine_grad",
            "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_clip_grads", "moe_cross_entropy_workspace_size",
            "moe_cross_entropy", "moe_cross_entropy_grad_workspace_size", "moe_cross_entropy_grad")
 
@@ -56,6 +57,12 @@ class MoeNorm(ctypes.Structure):
 
 class MoeMat(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class MoeFeedForward(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_rows", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("ld_dy", ctypes.c_int64), ("E", ctypes.c_int32), ("I", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("top_k", ctypes.c_int32), ("offsets", ctypes.c_void_p), ("perm", ctypes.c_void_p)]
 
 
 class MoeCombine(ctypes.Structure):
@@ -85,6 +92,7 @@ def lib() -> ctypes.CDLL:
         L = moe.lib()
         vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
         g, n, en, f32 = ctypes.POINTER(MoeGroups), ctypes.POINTER(MoeNorm), ctypes.c_int, ctypes.c_float
+        ff = ctypes.POINTER(MoeFeedForward)
         c, t, l = ctypes.POINTER(MoeCombine), ctypes.POINTER(MoeTensor), ctypes.POINTER(MoeLoss)
         sig = {
             "moe_grouped_matmul": (en, [g, vp, vp, vp, en, vp]),
@@ -101,6 +109,8 @@ def lib() -> ctypes.CDLL:
             "moe_norm_grad_workspace_size": (sz, [n]),
             "moe_gated_matmul": (en, [g, vp, vp, vp, MoeMat, vp]),
             "moe_gated_matmul_grad": (en, [g, vp, vp, MoeMat, MoeMat, vp, vp]),
+            "moe_feed_forward_grad_workspace_size": (sz, [ff]),
+            "moe_feed_forward_grad": (en, [ff, vp, vp, vp, vp, MoeMat, MoeMat, vp, vp, en, vp, sz, vp]),
             "moe_invert_permutation": (en, [i64, vp, vp, i32, i64, vp, vp]),
             "moe_combine": (en, [c, MoeMat, vp, MoeMat, MoeMat, vp]),
             "moe_combine_grad": (en, [c, MoeMat, MoeMat, vp, MoeMat, vp, vp]),
@@ -318,16 +328,14 @@ def feed_forward(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
 
 def feed_forward_grad(dy: torch.Tensor, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
                       gate_up: torch.Tensor, offsets: Optional[torch.Tensor], perm: Optional[torch.Tensor] = None,
-                      top_k: int = 1, dw_dtype: torch.dtype = torch.float32, stream=None) -> dict:
-    """The gradients of :func:`feed_forward` from dy (bf16 [rows, H]) and the gate_up that it saved, as a
-    dict: ``x`` (bf16, of each grouped row: :func:`combine` with top_k sums a token's), ``w_gate_up``
-    and ``w_down`` (in dw_dtype; zeros for an expert without rows).  The gradient of gate_up and h are
-    rounded to bf16 between the kernels."""
-    g = gated_matmul_grad(dy, w_down, gate_up, offsets, stream)
-    return dict(x=grouped_matmul_grad_input(g["gate_up"], w_gate_up, offsets, stream=stream),
-                w_gate_up=grouped_matmul_grad_weight(x, g["gate_up"], offsets, perm, top_k, out_dtype=dw_dtype,
-                                                     stream=stream),
-                w_down=grouped_matmul_grad_weight(g["h"], dy, offsets, out_dtype=dw_dtype, stream=stream))
+                      top_k: int = 1, dw_dtype: torch.dtype = torch.float32,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """moe_feed_forward_grad: the gradients of :func:`feed_forward` from dy (bf16 [rows, H]) and the gate_up
+    that it saved, as a dict: ``x`` (bf16, of each grouped row: :func:`combine` with top_k sums a
+    token's), ``w_gate_up`` and ``w_down`` (in dw_dtype; zeros for an expert without rows).  The
+    gradient of gate_up and h are rounded to bf16 between the kernels."""
+    return _call(stream, _ops.feed_forward_grad, dy, x, w_gate_up, w_down, gate_up, offsets, perm, top_k,
+                 _fp32(dw_dtype), workspace)
 
 
 # ------------------------------------------------------------------ combine

@@ -70,6 +70,46 @@ def test_gated_products_refuse_pointers():
     assert ggrad(g, h=at(4)) == INVALID
 
 
+def ffn(rows=100, x_rows=50, ldx=64, ld_dy=96, E=4, I=128, K=64, H=96, top_k=2, offsets=at(10), perm=at(11)):
+    return ops.MoeFeedForward(rows, x_rows, ldx, ld_dy, E, I, K, H, top_k, offsets, perm)
+
+
+def fgrad(d, dy=at(0), x=at(1), wg=at(2), wd=at(3), gu=mat(4, 256), dx=mat(5, 64), dg=at(6), dd=at(7), t=0, wk=at(8),
+          wkb=1 << 40):
+    return ops.lib().moe_feed_forward_grad(None if d is None else ctypes.byref(d), dy, x, wg, wd, gu, dx, dg, dd, t, wk,
+                                           wkb, None)
+
+
+def test_feed_forward_gradient_refuses():
+    size = ops.lib().moe_feed_forward_grad_workspace_size
+    assert fgrad(None) == INVALID and fgrad(ffn(rows=-1)) == INVALID and fgrad(ffn(x_rows=-1)) == INVALID
+    for bad in (dict(rows=1 << 31), dict(I=12), dict(I=0), dict(I=-8), dict(I=16392), dict(I=1 << 30), dict(K=60),
+                dict(K=16392, ldx=16392), dict(H=12), dict(H=0), dict(E=0), dict(E=1025), dict(top_k=0),
+                dict(ld_dy=(1 << 20) + 8), dict(x_rows=1 << 30)):
+        assert fgrad(ffn(**bad)) == SHAPE, bad
+        assert size(ctypes.byref(ffn(**bad))) == 0, bad
+    assert fgrad(ffn(ldx=56)) == INVALID and fgrad(ffn(ld_dy=88)) == INVALID and fgrad(ffn(offsets=None)) == INVALID
+    assert fgrad(ffn(ldx=68)) == MISALIGNED and fgrad(ffn(ld_dy=100)) == MISALIGNED
+    assert fgrad(ffn(perm=None, x_rows=99)) == INVALID
+    d = ffn()
+    need = size(ctypes.byref(d))
+    assert need >= 100 * 3 * 128 * 2 and need % 256 == 0
+    assert fgrad(d, wkb=need - 1) == WS and fgrad(d, wk=at(8) + 16) == MISALIGNED
+    for n in ("dy", "x", "wg", "wd", "dg", "dd", "wk"):
+        assert fgrad(d, **{n: None}) == INVALID, n
+    for n in ("dy", "x", "wg", "wd", "dg", "dd"):
+        assert fgrad(d, **{n: at(9) + 8}) == MISALIGNED, n
+    assert fgrad(d, gu=mat(None)) == INVALID and fgrad(d, gu=mat(4, 248)) == INVALID and fgrad(d, gu=mat(4, 260)) == MISALIGNED
+    assert fgrad(d, dx=mat(None)) == INVALID and fgrad(d, dx=mat(5, 56)) == INVALID
+    assert fgrad(d, dx=mat(5, (1 << 20) + 8)) == SHAPE
+    assert fgrad(d, t=2) == INVALID
+    for n, i in (("dx", mat(0, 64)), ("dg", at(2)), ("dd", at(7)), ("wk", at(4))):
+        assert fgrad(d, **{n: i, **({"dg": at(7)} if n == "dd" else {})}) == INVALID, n
+    # few experts, long groups: parts of the weight gradients in the workspace
+    one = ffn(rows=4096, x_rows=4096, E=1, offsets=None, perm=None)
+    assert size(ctypes.byref(one)) > 4096 * 3 * 128 * 2 + 2 * (256 * 64 + 96 * 128) * 4
+
+
 def comb(tokens=10, rows=20, H=64, k=2, E=4, t=0, inverse=at(6), perm=at(7), offsets=None):
     return ops.MoeCombine(tokens, rows, H, k, E, t, inverse, perm, offsets)
 

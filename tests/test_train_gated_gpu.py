@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import train_util as U
-from ops_util import F8, close, eps_of, grad_input_ref, grad_weight_ref, offsets_of, randn, source_rows, take
+from ops_util import F8, close, eps_of, grad_input_ref, grad_weight_ref, grouped_ref, offsets_of, randn, source_rows, take
 from sparse_moe_router_amd import ops
 
 pytestmark = pytest.mark.gpu
@@ -121,17 +121,21 @@ def test_infinities_and_nan_stay_in_their_rows():
 
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("dw", [BF16, F32])
-def test_block_and_its_gradients(gather, dw):
-    """Each kernel of the block against 64 bits on the values that the kernels before it stored."""
-    counts, I, K, H = [70, 0, 261, 5, 1], 72, 136, 136
+@pytest.mark.parametrize("counts,I,K,H", [([70, 0, 261, 5, 1], 72, 136, 136), ([3001], 40, 72, 24), ([1500, 0, 700], 264, 40, 72),
+                                          ([520] * 20, 16, 264, 8), ([9000], 8, 8, 264)], ids=lambda v: str(v)[:24])
+def test_block_and_its_gradients(gather, dw, counts, I, K, H):
+    """Each kernel of the block against 64 bits on the values that the kernels before it stored; few experts with
+    long groups, whose weight gradients are summed in parts, among them."""
     x, w, off, perm, k = inputs(counts, I, K, gather)
     R, E = sum(counts), len(counts)
     wd, dy = randn(8, E, H, I, scale=0.1), randn(9, R, H)
+    ffn = ops.MoeFeedForward(R, x.shape[0], K, H, E, I, K, H, k, 1 << 20, 1 << 24 if gather else None)
+    parts = ops.lib().moe_feed_forward_grad_workspace_size(ffn) - sum((n + 255) // 256 * 256 for n in (R * 4 * I, R * 2 * I))
+    assert (parts > 0) == (R >= 512 * E)
     c = lambda t: None if t is None else t.cuda()
     y, gu = ops.feed_forward(c(x), c(w), c(wd), c(off), perm=c(perm), top_k=k, save=True)
     assert torch.equal(y, ops.feed_forward(c(x), c(w), c(wd), c(off), perm=c(perm), top_k=k))
     h = ops.gated_matmul(c(x), c(w), c(off), perm=c(perm), top_k=k).cpu().to(F8)
-    from ops_util import grouped_ref
     want, t = grouped_ref(h, wd, off)
     close(y, want, t + eps_of(BF16) * want.abs())
     g = ops.feed_forward_grad(c(dy), c(x), c(w), c(wd), gu, c(off), perm=c(perm), top_k=k, dw_dtype=dw)
