@@ -165,6 +165,21 @@ struct LossArgs {
   bool dx32, dw32;
   void* dw;  // or NULL
 };
+// The tokens as the kernels of the logits take them.
+struct LossTokens {
+  const int64_t* target;
+  int64_t ignore;
+  int V, v0;      // vocabulary; first column of the piece
+  float2* part;   // forward: [panel][rows] maximum, sum of exp(z - maximum)
+  float* hit;     // forward: [rows] z at the target
+  const float *lse, *d_loss;  // gradient
+  uint16_t* d;                // gradient: [rows][ldd]
+  int64_t ldd;
+};
+// The logits of few tokens: 16 columns a workgroup and a panel.
+constexpr int kSkinnyColumns = 16;
+hipError_t launch_loss_skinny(const Groups& g, const void* x, const void* w, const LossTokens& loss, bool grad,
+                              hipStream_t s);
 // The gradient goes through the vocabulary in pieces whose d (bf16) takes at most kLossPieceBytes,
 // but at least kLossPieceColumns columns; dx is summed in `slices` buffers, each over `slice` columns
 // of a piece.

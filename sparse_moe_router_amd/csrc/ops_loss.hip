@@ -6,8 +6,7 @@
 // Forward: every 256 x 256 tile of z is reduced in its epilogue to a maximum
 // and a sum of exponentials for each row, 8 bytes where z has 1024; a second
 // launch joins the panels of a row.  Gradients: the vocabulary goes by in
-// pieces; a piece's z is computed again (the same sums in the same order as in
-// the forward call), becomes d in bf16 in the epilogue, and d feeds the two
+// pieces; a piece's z is computed again, becomes d in bf16 in the epilogue, and d feeds the two
 // gradient products of the piece while it is still in the last-level cache.
 // dx is summed over the pieces in fp32; where its tiles are too few for the
 // chip, a piece's reduction is cut into slices with sums of their own, which
@@ -19,6 +18,8 @@
 // of which 0.17% is the rounding of the results).  dx takes d_loss in fp32 with
 // its last sum; dW takes the largest d_loss in its epilogue, and the token's
 // share of that, exactly 1 for a mean, into the bf16 copy of x that it reads.
+#include "ops_loss.h"
+#include "ops_paths.h"
 #include "ops_sum.h"
 #include "ops_tile.h"
 
@@ -26,9 +27,6 @@ namespace moe {
 namespace {
 
 constexpr float LOG2E = 1.44269504088896340736f;
-
-// exp(x - m), 0 where both are -inf.
-__device__ __forceinline__ float exp_from(float x, float m) { return x == -INFINITY ? 0.0f : __expf(x - m); }
 
 // The value of lane i ^ 1, i ^ 2 of each four.
 __device__ __forceinline__ float quad_xor1(float v) {
@@ -40,10 +38,8 @@ __device__ __forceinline__ float quad_xor2(float v) {
 
 struct LseEpi {
   static constexpr bool kGated = false;
-  const int64_t* target;
-  int64_t rows;   // of all tiles
-  float2* part;   // [panel][rows] maximum, sum of exp(z - maximum)
-  float* hit;     // [rows] z at the target, where a tile has it
+  LossTokens t;
+  int64_t rows;  // of all tiles
 
   template <int RB0, int RB1, class ACC>
   __device__ __forceinline__ void tile(const TileArgs& p, const TileOut& o, ACC& acc, u32x4_t* lds) const {
@@ -55,11 +51,11 @@ struct LseEpi {
     float2 mine[NB][2];  // of the lane's row in each half block
     int b = 0;
     each_block<RB0, RB1>(o, acc, [&](int row0, const f32x16_t& a0, const f32x16_t& a1) __attribute__((always_inline)) {
-      int64_t t[2];
+      int64_t at[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int row = row0 + 16 * q + (o.lane >> 2);
-        t[q] = row < o.rows ? target[o.p0 + row] - col : -1;
+        at[q] = row < o.rows ? t.target[o.p0 + row] - col : -1;
       }
       // both halves are read before either is reduced: their chains of exchanges overlap
       float v[2][16];
@@ -74,8 +70,8 @@ struct LseEpi {
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[q][4 * i + k] = x[k];
         }
-        if (t[q] >= 0 && t[q] < 16 && t[q] < n)
-          hit[o.p0 + row0 + 16 * q + row] = ((const float*)staged(st, row, 4 * side + ((int)t[q] >> 2)))[t[q] & 3];
+        if (at[q] >= 0 && at[q] < 16 && at[q] < n)
+          t.hit[o.p0 + row0 + 16 * q + row] = ((const float*)staged(st, row, 4 * side + ((int)at[q] >> 2)))[at[q] & 3];
         wave_sync();
       }
       if (!whole)
@@ -123,7 +119,7 @@ struct LseEpi {
     for (int w = 0; w < 4; ++w) m = fmaxf(m, sums[w * TB + o.tid].x);
 #pragma unroll
     for (int w = 0; w < 4; ++w) s += sums[w * TB + o.tid].y * exp_from(sums[w * TB + o.tid].x, m);
-    part[o.panel * rows + o.p0 + o.tid] = float2{m, s};
+    t.part[o.panel * rows + o.p0 + o.tid] = float2{m, s};
   }
 };
 
@@ -136,34 +132,37 @@ __global__ __launch_bounds__(512, 1) void k_loss_logits(TileArgs p, LseEpi epi) 
     row_tile<OP_NT, false, GX_ROWS>(p, lds, epi);
 }
 
-// Joins the panels of 16 rows, 16 threads a row.
-constexpr int JR = 16;
-__global__ __launch_bounds__(JR * 16) void k_loss_join(const float2* part, const float* hit, const int64_t* target,
-                                                       int64_t ignore, int64_t rows, int panels, int V, float* loss,
-                                                       float* lse) {
-  __shared__ float2 lds[16][JR];
+// Joins the panels of JR rows, 256 / JR threads a row: 16, or of few tokens one, whose panels are many.
+template <int JR>
+__global__ __launch_bounds__(256) void k_loss_join(LossTokens a, int64_t rows, int panels, float* loss, float* lse) {
+  constexpr int TH = 256 / JR;
+  __shared__ float2 lds[TH][JR];
   const int r = threadIdx.x % JR, j = threadIdx.x / JR;
   for (int64_t t0 = (int64_t)blockIdx.x * JR; t0 < rows; t0 += (int64_t)gridDim.x * JR) {
     const int64_t t = t0 + r;
     float m = -INFINITY, s = 0.0f;
     if (t < rows)
-      for (int i = j; i < panels; i += 16) {
-        const float2 q = part[i * rows + t];
+      for (int i = j; i < panels; i += TH) {
+        const float2 q = a.part[i * rows + t];
         const float b = fmaxf(m, q.x);
         s = s * exp_from(m, b) + q.y * exp_from(q.x, b);
         m = b;
       }
     __syncthreads();  // the rows before have been read
     lds[j][r] = float2{m, s};
-    __syncthreads();
+    for (int n = TH / 2; n > 0; n >>= 1) {
+      __syncthreads();
+      if (j < n) {
+        const float2 p = lds[j][r], q = lds[j + n][r];
+        const float b = fmaxf(p.x, q.x);
+        lds[j][r] = float2{b, p.y * exp_from(p.x, b) + q.y * exp_from(q.x, b)};
+      }
+    }
     if (j != 0 || t >= rows) continue;
-    for (int i = 1; i < 16; ++i) m = fmaxf(m, lds[i][r].x);
-    s = 0.0f;
-    for (int i = 0; i < 16; ++i) s += lds[i][r].y * exp_from(lds[i][r].x, m);
-    const float l = m + logf(s);
-    const int64_t g = target[t];
+    const float l = lds[0][r].x + logf(lds[0][r].y);
+    const int64_t g = a.target[t];
     if (lse) lse[t] = l;
-    loss[t] = g >= 0 && g < V && g != ignore ? l - hit[t] : 0.0f;
+    loss[t] = g >= 0 && g < a.V && g != a.ignore ? l - a.hit[t] : 0.0f;
   }
 }
 
@@ -174,10 +173,6 @@ __device__ __forceinline__ float larger(float a, float b) {
 
 // scale[t] = d_loss[t], 0 for a token without a target; *most = the one of largest magnitude, with its
 // sign, so that a d_loss that all tokens share is 1 of it.
-__device__ __forceinline__ float scale_of(const float* d_loss, const int64_t* target, int64_t ignore, int V, int64_t t) {
-  const int64_t g = target[t];
-  return g >= 0 && g < V && g != ignore ? d_loss[t] : 0.0f;
-}
 template <int WAVES>
 __device__ __forceinline__ float largest(float m, float* lds) {
 #pragma unroll
@@ -187,15 +182,14 @@ __device__ __forceinline__ float largest(float m, float* lds) {
   for (int i = 0; i < WAVES; ++i) m = larger(m, lds[i]);
   return m;
 }
-__global__ __launch_bounds__(1024) void k_loss_scale(const float* d_loss, const int64_t* target, int64_t ignore, int V,
-                                                     int64_t rows, float* scale, float* most) {
+__global__ __launch_bounds__(1024) void k_loss_scale(LossTokens a, int64_t rows, float* scale, float* most) {
   __shared__ float lds[16];
   float m = 0.0f;
 #pragma unroll 4
   for (int64_t t = threadIdx.x; t < rows; t += 1024) {
-    const float a = scale_of(d_loss, target, ignore, V, t);
-    scale[t] = a;
-    m = larger(m, a);
+    const float v = scale_of(a, t);
+    scale[t] = v;
+    m = larger(m, v);
   }
   m = largest<16>(m, lds);
   if (threadIdx.x == 0) *most = m;
@@ -205,17 +199,16 @@ __global__ __launch_bounds__(1024) void k_loss_scale(const float* d_loss, const 
 // tokens every workgroup finds the largest d_loss itself, which costs less than a launch before it.
 constexpr int kFewTokens = 2048;
 template <bool FEW>
-__global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* x, int64_t ldx, const float* d_loss,
-                                                   const int64_t* target, int64_t ignore, int V, int64_t rows,
+__global__ __launch_bounds__(256) void k_loss_rows(LossTokens a, const uint16_t* x, int64_t ldx, int64_t rows,
                                                    float* scale, float* most, int H, uint16_t* out) {
   __shared__ float lds[4];
   float m;
   if (FEW) {
     m = 0.0f;
     for (int64_t t = threadIdx.x; t < rows; t += 256) {
-      const float a = scale_of(d_loss, target, ignore, V, t);
-      if (blockIdx.x == 0) scale[t] = a;
-      m = larger(m, a);
+      const float v = scale_of(a, t);
+      if (blockIdx.x == 0) scale[t] = v;
+      m = larger(m, v);
     }
     m = largest<4>(m, lds);
     if (blockIdx.x == 0 && threadIdx.x == 0) *most = m;
@@ -226,7 +219,7 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* x, int64_t ld
   const int64_t n = rows * H;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 256 * 8) {
     const int64_t t = i / H;
-    const float a = FEW ? scale_of(d_loss, target, ignore, V, t) : scale[t], r = m != 0.0f ? a / m : a;
+    const float v = FEW ? scale_of(a, t) : scale[t], r = m != 0.0f ? v / m : v;
     const u32x4_t q = *(const u32x4_t*)(x + t * ldx + (i - t * H));
     u32x4_t o;
 #pragma unroll
@@ -237,12 +230,7 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* x, int64_t ld
 
 struct GradEpi {
   static constexpr bool kGated = false;
-  const int64_t* target;
-  int v0;  // first column of the piece
-  const float* lse;
-  const float* scale;  // 0: the token has no part
-  uint16_t* d;         // [rows][ldd]
-  int64_t ldd;
+  LossTokens t;
 
   template <int RB0, int RB1, class ACC>
   __device__ __forceinline__ void tile(const TileArgs& p, const TileOut& o, ACC& acc, u32x4_t* lds) const {
@@ -256,9 +244,9 @@ struct GradEpi {
       for (int i = 0; i < 4; ++i) {
         const int row = row0 + i * 8 + (o.lane >> 3);
         const int64_t grow = o.p0 + (row < o.rows ? row : 0);
-        hit[i] = target[grow] - v0 - col;
-        l[i] = -lse[grow] * LOG2E;
-        w[i] = scale[grow];
+        hit[i] = t.target[grow] - t.v0 - col;
+        l[i] = -t.lse[grow] * LOG2E;
+        w[i] = scale_of(t, grow);
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -281,7 +269,7 @@ struct GradEpi {
           if (!whole)
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = col + k < p.g.N ? v[k] : 0.0f;
-          *(u32x4_t*)(d + (o.p0 + row0 + 16 * q + row) * ldd + col) =
+          *(u32x4_t*)(t.d + (o.p0 + row0 + 16 * q + row) * t.ldd + col) =
               u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
         }
         wave_sync();
@@ -299,11 +287,16 @@ __global__ __launch_bounds__(512, 1) void k_loss_grad(TileArgs p, GradEpi epi) {
     row_tile<OP_NT, false, GX_ROWS>(p, lds, epi);
 }
 
-// Adds a tile to what earlier pieces left (add = 0: the first piece).
+// Adds a tile to what earlier pieces left (add = 0: the first piece).  With dx given (one piece, one slice)
+// the tile is dx already: times the token's d_loss and in its type.
 struct SumEpi {
   static constexpr bool kGated = false;
   float* out;  // [rows][K] of the slice
   int add;
+  void* dx;
+  int64_t lddx;
+  int dx32;
+  const float* scale;
 
   template <int RB0, int RB1, class ACC>
   __device__ __forceinline__ void tile(const TileArgs& p, const TileOut& o, ACC& acc, u32x4_t* lds) const {
@@ -325,7 +318,20 @@ struct SumEpi {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = 4 * q + j, row = j * 4 + (o.lane >> 4);
-          if (in[i]) *(f32x4_t*)(out + (o.p0 + row0 + 16 * q + row) * p.g.K + col) = was[i] + *staged(st, row, chunk);
+          if (!in[i]) continue;
+          const int64_t grow = o.p0 + row0 + 16 * q + row;
+          f32x4_t v = *staged(st, row, chunk);
+          if (!dx) {
+            *(f32x4_t*)(out + grow * p.g.K + col) = was[i] + v;
+            continue;
+          }
+          const float a = scale[grow];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] *= a;
+          if (dx32)
+            *(f32x4_t*)((float*)dx + grow * lddx + col) = v;
+          else
+            *(uint2*)((uint16_t*)dx + grow * lddx + col) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         }
         wave_sync();
       }
@@ -413,26 +419,46 @@ constexpr size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
+// Few tokens take the matrix-vector kernel, by the rule of the products: it does not wait for a tile's
+// whole reduction (2 tokens against 366 x 3400 38.6 us by tiles, 9.4 so; 20 against 442 x 3792 42 and 15).
+static bool few_logits(int64_t rows, int columns) { return takes_matrix_vector(rows, 1, columns); }
+static int loss_panels(int64_t rows, int V) {
+  const int w = few_logits(rows, V) ? kSkinnyColumns : TB;
+  return (V + w - 1) / w;
+}
+
 size_t loss_workspace(int64_t rows, int V) {
-  const int panels = (V + TB - 1) / TB;
-  return align256((size_t)panels * rows * sizeof(float2)) + align256((size_t)rows * 4);
+  return align256((size_t)loss_panels(rows, V) * rows * sizeof(float2)) + align256((size_t)rows * 4);
+}
+
+static LossTokens loss_tokens(const LossArgs& a) {
+  LossTokens t{};
+  t.target = a.target;
+  t.ignore = a.ignore;
+  t.V = a.V;
+  t.lse = a.lse;
+  t.d_loss = a.d_loss;
+  return t;
 }
 
 hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s) {
-  const int panels = (a.V + TB - 1) / TB;
-  float2* part = (float2*)workspace;
-  float* hit = (float*)((char*)workspace + align256((size_t)panels * a.rows * sizeof(float2)));
+  const int panels = loss_panels(a.rows, a.V);
+  LossTokens tokens = loss_tokens(a);
+  tokens.part = (float2*)workspace;
+  tokens.hit = (float*)((char*)workspace + align256((size_t)panels * a.rows * sizeof(float2)));
+  const Launch lc{s, nullptr, nullptr};
   TileArgs t{};
   t.g = one_matrix(a.rows, a.ldx, a.V, a.V, a.H);
   t.a = (const char*)a.x;
   t.b = (const char*)a.w;
   t.npan = panels;
-  const Launch lc{s, nullptr, nullptr};
-  hipError_t e = launch_rows(lc, k_loss_logits<true>, k_loss_logits<false>, t, LseEpi{a.target, a.rows, part, hit});
+  const bool few = few_logits(a.rows, a.V);
+  const hipError_t e = few ? launch_loss_skinny(t.g, a.x, a.w, tokens, false, s)
+                           : launch_rows(lc, k_loss_logits<true>, k_loss_logits<false>, t, LseEpi{tokens, a.rows});
   if (e != hipSuccess) return e;
-  const int64_t joins = (a.rows + JR - 1) / JR;
-  return launch(lc, k_loss_join, dim3((unsigned)(joins < (1 << 20) ? joins : 1 << 20)), dim3(JR * 16), (const float2*)part,
-                (const float*)hit, a.target, a.ignore, a.rows, panels, a.V, a.loss, a.lse_out);
+  const int64_t joins = few ? a.rows : (a.rows + 15) / 16;
+  return launch(lc, few ? k_loss_join<1> : k_loss_join<16>, dim3((unsigned)(joins < (1 << 20) ? joins : 1 << 20)),
+                dim3(256), tokens, a.rows, panels, a.loss, a.lse_out);
 }
 
 LossPlan loss_plan(int64_t rows, int V, int H) {
@@ -473,17 +499,19 @@ hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
   const Launch lc{s, nullptr, nullptr};
   const int64_t total = a.rows * a.H, groups = (total / 8 + 255) / 256;
   const dim3 each((unsigned)(groups < 1024 ? groups : 1024));
+  LossTokens tokens = loss_tokens(a);
+  tokens.d = d;
+  tokens.ldd = plan.piece;
   if (a.rows > 0) {
     const bool few = a.rows <= kFewTokens;
     hipError_t e = hipSuccess;
-    if (!few)
-      e = launch(lc, k_loss_scale, dim3(1), dim3(1024), a.d_loss, a.target, a.ignore, a.V, a.rows, scale, most);
+    if (!few) e = launch(lc, k_loss_scale, dim3(1), dim3(1024), tokens, a.rows, scale, most);
     if (e == hipSuccess && (few || a.dw))
-      e = launch(lc, few ? k_loss_rows<true> : k_loss_rows<false>, few && !a.dw ? dim3(1) : each, dim3(256),
-                 (const uint16_t*)a.x, a.ldx, a.d_loss, a.target, a.ignore, a.V, a.rows, scale, most, a.H,
-                 a.dw ? x : nullptr);
+      e = launch(lc, few ? k_loss_rows<true> : k_loss_rows<false>, few && !a.dw ? dim3(1) : each, dim3(256), tokens,
+                 (const uint16_t*)a.x, a.ldx, a.rows, scale, most, a.H, a.dw ? x : nullptr);
     if (e != hipSuccess) return e;
   }
+  const bool direct = plan.slices == 1 && plan.piece >= a.V;
   for (int64_t v0 = 0; v0 < a.V; v0 += plan.piece) {
     const int n = (int)(a.V - v0 < plan.piece ? a.V - v0 : plan.piece);
     const char* w = (const char*)a.w + v0 * a.H * 2;
@@ -494,15 +522,16 @@ hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
     t.npan = (n + TB - 1) / TB;
     hipError_t e = hipSuccess;
     if (a.rows > 0) {
-      e = launch_rows(lc, k_loss_grad<true>, k_loss_grad<false>, t,
-                      GradEpi{a.target, (int)v0, a.lse, scale, d, (int64_t)plan.piece});
+      tokens.v0 = (int)v0;
+      e = few_logits(a.rows, n) ? launch_loss_skinny(t.g, a.x, w, tokens, true, s)
+                                : launch_rows(lc, k_loss_grad<true>, k_loss_grad<false>, t, GradEpi{tokens});
       if (e != hipSuccess) return e;
     }
     LossTiles f{};
     f.dx = t;
     f.dx.a = (const char*)d;
     f.dx.npan = (a.H + TB - 1) / TB;
-    f.sum = SumEpi{part, v0 > 0};
+    f.sum = SumEpi{part, v0 > 0, direct ? a.dx : nullptr, a.lddx, (int)a.dx32, scale};
     f.slice = plan.slice;
     f.slices = plan.slices;
     f.row_tiles = (int)((a.rows + TB - 1) / TB);
@@ -526,7 +555,7 @@ hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
       e = launch_sum_parts(dw_part, plan.splits, (int64_t)n * a.H, most, dw, a.dw32, s);
     if (e != hipSuccess) return e;
   }
-  if (!a.dx || a.rows == 0) return hipSuccess;
+  if (!a.dx || a.rows == 0 || direct) return hipSuccess;
   return launch(lc, k_loss_dx_sum, each, dim3(256), (const float*)part, plan.slices, total, a.H, a.lddx,
                 (const float*)scale, a.dx, (int)a.dx32);
 }

@@ -13,10 +13,13 @@
 // bf16 for int8 weights are quantised by every workgroup for itself while its
 // first weights are on their way, when they are few: a launch of its own and
 // its results' way through memory cost more.  Gated products take eight rows of
-// each of the expert's two matrices, whose sums then meet in the same place.
+// each of the expert's two matrices, whose sums then meet in the same place.  The
+// logits of few tokens against a vocabulary become a maximum and a sum of
+// exponentials of each token and 16 columns, or their gradients, there.
 #include <type_traits>
 
 #include "ops_internal.h"
+#include "ops_loss.h"
 #include "ops_paths.h"
 #include "quantize8.h"
 
@@ -39,6 +42,7 @@ struct SkinnyArgs {
   int fp32;
   uint16_t* pre;  // gated: the products themselves (NULL: not kept)
   int64_t ldp;
+  LossTokens loss;  // logits
   int by_row;  // workgroup row = row of the grouped order (else the expert)
 };
 
@@ -86,13 +90,15 @@ __device__ __forceinline__ void quantize_rows(const SkinnyArgs& p, int64_t p0, i
   __syncthreads();
 }
 
-// QX: x is bf16 and quantised here (rows <= QR, NB = 1).  GATED: n0 counts the
+enum { PLAIN = 0, GATED_UNIT = 1, LOGITS = 2, LOGIT_GRADS = 3 };
+// QX: x is bf16 and quantised here (rows <= QR, NB = 1).  GATED_UNIT: n0 counts the
 // rows of each matrix; the block's rows 0..7 are of the first, 8..15 of the second.
-template <bool I8, int NB, bool QX, bool GATED>
+template <bool I8, int NB, bool QX, int MODE>
 __device__ __forceinline__ void skinny_block(const SkinnyArgs& p, int e, int n0, int64_t p0, int rows, float* red,
                                              int8_t* codes, float* qscale) {
   typedef typename std::conditional<I8, i32x4_t, f32x4_t>::type acc_t;
   constexpr int ES = I8 ? 1 : 2;
+  constexpr bool GATED = MODE == GATED_UNIT;
   const Groups& g = p.g;
   const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -184,6 +190,32 @@ __device__ __forceinline__ void skinny_block(const SkinnyArgs& p, int e, int n0,
     }
     return;
   }
+  if constexpr (MODE == LOGITS || MODE == LOGIT_GRADS) {
+    for (int i = threadIdx.x; i < (rows + 3) / 4 * 64; i += 64 * SW) {  // a column a thread, a token 16 lanes
+      const int r = i >> 4, c = i & 15, col = n0 + c;
+      if (r >= rows) continue;
+      float z = 0.0f;
+#pragma unroll
+      for (int w = 0; w < SW; ++w) z += rd[(w * 16 * NB + r) * 16 + c];
+      const int64_t t = p0 + r, hit = p.loss.target[t] - p.loss.v0;
+      if constexpr (MODE == LOGITS) {
+        if (col >= g.N) z = -INFINITY;
+        if (hit == col) p.loss.hit[t] = z;
+        float m = z;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+        float e = exp_from(z, m);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) e += __shfl_xor(e, d, 64);
+        if (c == 0) p.loss.part[(int64_t)blockIdx.x * g.rows + t] = float2{m, e};
+      } else {
+        // all 16 columns: those past the vocabulary, which the products read with the last eight, are zeros
+        const float w = scale_of(p.loss, t), e = __expf(z - p.loss.lse[t]);
+        p.loss.d[t * p.loss.ldd + col] = (uint16_t)f32_to_bf16(w != 0.0f && col < g.N ? (hit == col ? e - 1.0f : e) : 0.0f);
+      }
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < rows * 8; i += 64 * SW) {  // two weight rows a thread
     const int r = i >> 3, c = 2 * (i & 7), col = n0 + c;
     if (col >= g.N) continue;
@@ -211,13 +243,13 @@ __device__ __forceinline__ void skinny_block(const SkinnyArgs& p, int e, int n0,
   }
 }
 
-template <bool I8, bool QX, bool GATED = false>
+template <bool I8, bool QX, int MODE = PLAIN>
 __global__ __launch_bounds__(64 * SW) void k_op_skinny(SkinnyArgs p) {
   __shared__ float red[QX ? SW * 16 * 16 : SW * 64 * 16];
   __shared__ float qscale[QR];
   extern __shared__ u32x4_t codes[];  // QX: QR rows of K + 16 bytes
   const Groups& g = p.g;
-  const int n0 = blockIdx.x * (GATED ? SN / 2 : SN);
+  const int n0 = blockIdx.x * (MODE == GATED_UNIT ? SN / 2 : SN);
   int e = blockIdx.y;
   if (p.by_row) {
     // the expert of row blockIdx.y, taken by the workgroup of its first row
@@ -237,11 +269,11 @@ __global__ __launch_bounds__(64 * SW) void k_op_skinny(SkinnyArgs p) {
     constexpr int MAXR = QX ? QR : 64;
     const int rows = (int)(hi - lo < MAXR ? hi - lo : MAXR);
     if (QX || rows <= 16)
-      skinny_block<I8, 1, QX, GATED>(p, e, n0, lo, rows, red, (int8_t*)codes, qscale);
+      skinny_block<I8, 1, QX, MODE>(p, e, n0, lo, rows, red, (int8_t*)codes, qscale);
     else if (rows <= 32)
-      skinny_block<I8, 2, false, GATED>(p, e, n0, lo, rows, red, nullptr, nullptr);
+      skinny_block<I8, 2, false, MODE>(p, e, n0, lo, rows, red, nullptr, nullptr);
     else
-      skinny_block<I8, 4, false, GATED>(p, e, n0, lo, rows, red, nullptr, nullptr);
+      skinny_block<I8, 4, false, MODE>(p, e, n0, lo, rows, red, nullptr, nullptr);
     lo += rows;
     if (lo < hi) __syncthreads();  // the partial sums are read before they are overwritten
   }
@@ -260,7 +292,20 @@ hipError_t launch_gated_skinny(const Groups& g, const void* x, const void* w, vo
   a.ldp = ldp;
   a.by_row = g.offsets && g.rows < g.E;
   const dim3 grid((unsigned)((g.N + SN / 2 - 1) / (SN / 2)), (unsigned)(a.by_row ? g.rows : g.E));
-  return launch(Launch{s, nullptr, nullptr}, k_op_skinny<false, false, true>, grid, dim3(64 * SW), a);
+  return launch(Launch{s, nullptr, nullptr}, k_op_skinny<false, false, GATED_UNIT>, grid, dim3(64 * SW), a);
+}
+
+hipError_t launch_loss_skinny(const Groups& g, const void* x, const void* w, const LossTokens& loss, bool grad,
+                              hipStream_t s) {
+  SkinnyArgs a{};
+  a.g = g;
+  a.x = (const char*)x;
+  a.w = (const char*)w;
+  a.loss = loss;
+  const dim3 grid((unsigned)((g.N + SN - 1) / SN), 1);
+  const Launch lc{s, nullptr, nullptr};
+  return grad ? launch(lc, k_op_skinny<false, false, LOGIT_GRADS>, grid, dim3(64 * SW), a)
+              : launch(lc, k_op_skinny<false, false, LOGITS>, grid, dim3(64 * SW), a);
 }
 
 hipError_t launch_op_skinny(bool i8, bool quantize, const Groups& g, const void* x, const void* w, const Scales& sc, void* y,
