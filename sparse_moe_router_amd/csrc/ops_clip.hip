@@ -8,8 +8,8 @@
 // its bytes, and no size of a gradient overflows or vanishes in them.
 //
 // The tensors' addresses travel as arguments of the launch, so that a call needs
-// no copy to the device and may be captured; they are cut into pieces of 32768
-// elements that the workgroups take in turn.  The scaling pass goes backwards:
+// no copy to the device and may be captured; they are cut into pieces of 2048 to
+// at most 32768 elements that the workgroups take in turn.  The scaling pass goes backwards:
 // what the first one read last is still in the last-level cache.
 #include "ops_internal.h"
 
@@ -18,7 +18,6 @@ namespace {
 
 constexpr int CT = 256;           // threads
 constexpr int CU = 4;             // 16-byte loads of a thread in flight
-constexpr int64_t PIECE = 32768;  // elements
 
 // sum over the workgroup; all threads get it
 __device__ __forceinline__ double block_sum(double v, double* lds) {
@@ -33,17 +32,52 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return v;
 }
 
-// The tensor that holds piece i.
-__device__ __forceinline__ int find_tensor(const GradTable& t, int64_t i) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (t.first[mid] <= i)
-      lo = mid;
-    else
-      hi = mid - 1;
+// The table, the launch's first argument, two tensors a lane: one way to memory for all of it, where a
+// search over the arguments takes one a step (61 tensors of 400 thousand elements in all: 6.5 and 7.7 us
+// with it, 5.5 and 6.7 without).
+struct Table {
+  const char* in[2];
+  char* out[2];
+  int64_t n[2];
+  int32_t first[2];
+  uint32_t types[2];  // bit 0: in is fp32, bit 1: out
+  int count;
+};
+__device__ __forceinline__ Table read_table(int count) {
+  const GradTable* g = (const GradTable*)(const char*)__builtin_amdgcn_kernarg_segment_ptr();
+  Table t;
+  t.count = count;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = (int)(threadIdx.x & 63) + 64 * u, j = i < count ? i : 0;
+    t.in[u] = (const char*)g->in[j];
+    t.out[u] = (char*)g->out[j];
+    t.n[u] = g->n[j];
+    t.first[u] = i < count ? g->first[j] : 0x7FFFFFFF;
+    t.types[u] = (g->types[0][j >> 5] >> (j & 31) & 1) | (g->types[1][j >> 5] >> (j & 31) & 1) << 1;
   }
-  return lo;
+  return t;
+}
+__device__ __forceinline__ int64_t pick(const int64_t (&v)[2], int j) {
+  const int64_t x = j < 64 ? v[0] : v[1];
+  return ((int64_t)__builtin_amdgcn_readlane((int)(x >> 32), j & 63) << 32) |
+         (uint32_t)__builtin_amdgcn_readlane((int)x, j & 63);
+}
+// Elements [a, b) of the tensor that piece i is of.
+struct Piece {
+  const void* in;
+  void* out;
+  int64_t a, b;
+  bool in32, out32;
+};
+__device__ __forceinline__ Piece find_piece(const Table& t, int i, int shift) {
+  const int j = __builtin_popcountll(__ballot(t.first[0] <= i)) + __builtin_popcountll(__ballot(t.first[1] <= i)) - 1;
+  const int64_t n = pick(t.n, j), in[2] = {(int64_t)t.in[0], (int64_t)t.in[1]},
+                out[2] = {(int64_t)t.out[0], (int64_t)t.out[1]};
+  const int first = __builtin_amdgcn_readlane(j < 64 ? t.first[0] : t.first[1], j & 63);
+  const uint32_t types = (uint32_t)__builtin_amdgcn_readlane((int)(j < 64 ? t.types[0] : t.types[1]), j & 63);
+  const int64_t a = (int64_t)(i - first) << shift, b = a + ((int64_t)1 << shift);
+  return Piece{(const void*)pick(in, j), (void*)pick(out, j), a, b < n ? b : n, (types & 1) != 0, (types & 2) != 0};
 }
 
 template <class T>
@@ -101,13 +135,13 @@ __device__ __forceinline__ double squares(const T* p, int64_t a, int64_t b) {
   return s;
 }
 
-__global__ __launch_bounds__(CT) void k_squares(GradTable t, double* part) {
+__global__ __launch_bounds__(CT) void k_squares(GradTable g, double* part) {
   __shared__ double lds[CT / 64];
   double s = 0.0;
-  for (int64_t i = blockIdx.x; i < t.pieces; i += gridDim.x) {
-    const int j = find_tensor(t, i);
-    const int64_t a = (i - t.first[j]) * PIECE, b = a + PIECE < t.n[j] ? a + PIECE : t.n[j];
-    s += t.type(j, 0) ? squares((const float*)t.in[j], a, b) : squares((const uint16_t*)t.in[j], a, b);
+  const Table t = read_table(g.count);
+  for (int i = blockIdx.x; i < g.pieces; i += gridDim.x) {
+    const Piece p = find_piece(t, i, g.shift);
+    s += p.in32 ? squares((const float*)p.in, p.a, p.b) : squares((const uint16_t*)p.in, p.a, p.b);
   }
   s = block_sum(s, lds);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -176,9 +210,10 @@ __device__ __forceinline__ void scale(const TI* in, TO* out, int64_t a, int64_t 
 }
 
 // part NULL: *norm is given; else the norm is the root of their sum, and stored by the first workgroup.
-__global__ __launch_bounds__(CT) void k_clip(GradTable t, const double* part, int parts, float* norm, float max_norm,
+__global__ __launch_bounds__(CT) void k_clip(GradTable g, const double* part, int parts, float* norm, float max_norm,
                                              float eps, int store) {
   __shared__ double lds[CT / 64];
+  const Table t = read_table(g.count);
   float r;
   if (part) {
     r = (float)sqrt(join(part, parts, lds));
@@ -188,26 +223,31 @@ __global__ __launch_bounds__(CT) void k_clip(GradTable t, const double* part, in
   }
   const double q = (double)max_norm / ((double)r + (double)eps);
   const float c = q >= 1.0 ? 1.0f : (float)q;  // a NaN stays one
-  for (int64_t k = blockIdx.x; k < t.pieces; k += gridDim.x) {
-    const int64_t i = t.pieces - 1 - k;
-    const int j = find_tensor(t, i);
-    if (c == 1.0f && t.in[j] == t.out[j]) continue;  // as it is
-    const int64_t a = (i - t.first[j]) * PIECE, b = a + PIECE < t.n[j] ? a + PIECE : t.n[j];
-    const bool fi = t.type(j, 0), fo = t.type(j, 1);
-    if (fi && fo)
-      scale((const float*)t.in[j], (float*)t.out[j], a, b, c);
-    else if (fi)
-      scale((const float*)t.in[j], (uint16_t*)t.out[j], a, b, c);
-    else if (fo)
-      scale((const uint16_t*)t.in[j], (float*)t.out[j], a, b, c);
+  for (int k = blockIdx.x; k < g.pieces; k += gridDim.x) {
+    const Piece p = find_piece(t, g.pieces - 1 - k, g.shift);
+    if (c == 1.0f && p.in == p.out) continue;  // as it is
+    if (p.in32 && p.out32)
+      scale((const float*)p.in, (float*)p.out, p.a, p.b, c);
+    else if (p.in32)
+      scale((const float*)p.in, (uint16_t*)p.out, p.a, p.b, c);
+    else if (p.out32)
+      scale((const uint16_t*)p.in, (float*)p.out, p.a, p.b, c);
     else
-      scale((const uint16_t*)t.in[j], (uint16_t*)t.out[j], a, b, c);
+      scale((const uint16_t*)p.in, (uint16_t*)p.out, p.a, p.b, c);
   }
 }
 
 }  // namespace
 
-int64_t clip_pieces(int64_t n) { return (n + PIECE - 1) / PIECE; }
+int64_t clip_pieces(int64_t n, int shift) { return (n + ((int64_t)1 << shift) - 1) >> shift; }
+// As large as leaves every one of the kClipGroups workgroups a piece: a workgroup goes through one in
+// steps that wait for each other (61 tensors of 400 thousand elements in all: pieces of 32768 5.5 and
+// 6.7 us, of 2048 3.5 and 3.9).
+int clip_shift(int64_t elements) {
+  int shift = 11;
+  while (shift < 15 && (elements >> shift) > kClipGroups) ++shift;
+  return shift;
+}
 int clip_groups(int64_t pieces) { return (int)(pieces < kClipGroups ? pieces : kClipGroups); }
 
 hipError_t launch_squares(const GradTable& t, double* part, hipStream_t s) {

@@ -140,10 +140,11 @@ struct GradTable {
   uint32_t types[2][4];         // bit j: tensor j of in (0) or out (1) is fp32
   int32_t count;
   int32_t pieces;
-  __host__ __device__ bool type(int j, int of_out) const { return types[of_out][j >> 5] >> (j & 31) & 1; }
+  int32_t shift;                // elements of a piece: 2^shift
 };
-static_assert(sizeof(GradTable) < 3840, "kernel arguments");
-int64_t clip_pieces(int64_t n);
+static_assert(kClipTensors <= 128 && sizeof(GradTable) < 3840, "kernel arguments");
+int64_t clip_pieces(int64_t n, int shift);
+int clip_shift(int64_t elements);  // of all tensors of a call
 int clip_groups(int64_t pieces);
 hipError_t launch_squares(const GradTable& t, double* part, hipStream_t s);
 hipError_t launch_norm(const double* part, int parts, float* norm, hipStream_t s);

@@ -251,18 +251,36 @@ __global__ __launch_bounds__(64 * SW) void k_op_skinny(SkinnyArgs p) {
   const Groups& g = p.g;
   const int n0 = blockIdx.x * (MODE == GATED_UNIT ? SN / 2 : SN);
   int e = blockIdx.y;
+  Range range;
   if (p.by_row) {
-    // the expert of row blockIdx.y, taken by the workgroup of its first row
+    // the expert of row blockIdx.y, taken by the workgroup of its first row; of up to 256 experts all
+    // offsets are on their way at a time, and the expert's own are among them
     const int64_t row = blockIdx.y;
     const int lane = threadIdx.x & 63;
+    const int32_t front = g.offsets[0];
+    int32_t v[4];
     e = 0;
-    for (int i = lane; i < (g.E + 63) / 64 * 64; i += 64)
-      e += __builtin_popcountll(__ballot(i < g.E && g.offsets[i + 1] <= row));
+    for (int i0 = 0; i0 < g.E; i0 += 256) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = g.offsets[i0 + 64 * u + lane < g.E ? i0 + 64 * u + lane + 1 : g.E];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) e += __builtin_popcountll(__ballot(i0 + 64 * u + lane < g.E && v[u] <= row));
+    }
     e = __builtin_amdgcn_readfirstlane(e);
     if (e >= g.E) return;
-    if (group_range(g, e).lo != row) return;
+    if (g.E <= 256) {
+      auto at = [&](int i) {  // offsets[i + 1]
+        const int32_t x = i < 64 ? v[0] : i < 128 ? v[1] : i < 192 ? v[2] : v[3];
+        return __builtin_amdgcn_readlane(x, i & 63);
+      };
+      range = limited(g, e > 0 ? at(e - 1) : front, at(e));
+    } else {
+      range = group_range(g, e);
+    }
+    if (range.lo != row) return;
+  } else {
+    range = group_range(g, e);
   }
-  const Range range = group_range(g, e);
   int64_t lo = range.lo;
   const int64_t hi = range.hi;
   while (lo < hi) {

@@ -91,6 +91,7 @@ moe_status_t check_tensors(const moe_tensor_t* t, int32_t count, bool outs) {
   return MOE_OK;
 }
 
+constexpr int64_t kClipPieces = 1 << 30;  // of a launch
 // Calls f(table) for the tensors, as many at a time as a launch takes.
 template <class F>
 moe_status_t each_table(const moe_tensor_t* t, int32_t count, bool outs, F&& f) {
@@ -102,10 +103,13 @@ moe_status_t each_table(const moe_tensor_t* t, int32_t count, bool outs, F&& f) 
       for (uint32_t& w : a) w = 0;
   };
   reset();
+  int64_t elements = 0;
+  for (int32_t i = 0; i < count; ++i) elements += t[i].n;
+  g.shift = clip_shift(elements);
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].n == 0) continue;
-    const int64_t pieces = clip_pieces(t[i].n);  // at most 2^25
-    if (g.count == kClipTensors || g.pieces + pieces > (1 << 30)) {
+    const int64_t pieces = clip_pieces(t[i].n, g.shift);  // at most 2^25
+    if (g.count == kClipTensors || g.pieces + pieces > kClipPieces) {
       const moe_status_t st = f(g);
       if (st != MOE_OK) return st;
       reset();
@@ -163,6 +167,25 @@ moe_status_t check_disjoint(const moe_tensor_t* t, int32_t count, bool outs, con
   return overlapping(x, n) ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 
+// Bytes of the parts of the sum of squares of checked tensors: each_table's launches.
+size_t parts_bytes(const moe_tensor_t* t, int32_t count) {
+  int64_t elements = 0, pieces = 0, parts = 0;
+  for (int32_t i = 0; i < count; ++i) elements += t[i].n;
+  const int shift = clip_shift(elements);
+  int tensors = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    const int64_t n = clip_pieces(t[i].n, shift);
+    if (tensors == kClipTensors || pieces + n > kClipPieces) {
+      parts += clip_groups(pieces);
+      tensors = 0, pieces = 0;
+    }
+    ++tensors, pieces += n;
+  }
+  parts += clip_groups(pieces);
+  return ((size_t)(parts > 0 ? parts : 1) * 8 + 255) & ~(size_t)255;
+}
+
 // The parts of the sum of squares into the workspace; their number.
 moe_status_t run_squares(const moe_tensor_t* t, int32_t count, double* part, int* parts, hipStream_t s) {
   *parts = 0;
@@ -173,11 +196,10 @@ moe_status_t run_squares(const moe_tensor_t* t, int32_t count, double* part, int
   });
 }
 
-moe_status_t check_norm_call(const moe_tensor_t* t, int32_t count, const float* norm, const void* workspace,
-                             size_t workspace_bytes) {
+moe_status_t check_norm_call(const float* norm, const void* workspace, size_t workspace_bytes, size_t need) {
   if (!norm || !workspace) return MOE_ERR_INVALID_ARG;
   if (!aligned(norm, 4) || !aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
-  return workspace_bytes < moe_grad_norm_workspace_size(t, count) ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+  return workspace_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
 moe_status_t check_loss(const moe_loss_t* d) {
@@ -393,20 +415,16 @@ moe_status_t moe_combine_grad(const moe_combine_t* d, moe_mat_t d_out, moe_mat_t
 }
 
 size_t moe_grad_norm_workspace_size(const moe_tensor_t* t, int32_t count) {
-  if (check_tensors(t, count, false) != MOE_OK) return 0;
-  size_t parts = 0;
-  each_table(t, count, false, [&](const GradTable& g) {
-    parts += (size_t)clip_groups(g.pieces);
-    return MOE_OK;
-  });
-  return ((parts > 0 ? parts : 1) * 8 + 255) & ~(size_t)255;
+  return check_tensors(t, count, false) == MOE_OK ? parts_bytes(t, count) : 0;
 }
 
 moe_status_t moe_grad_norm(const moe_tensor_t* t, int32_t count, float* norm, void* workspace, size_t workspace_bytes,
                            hipStream_t stream) {
   moe_status_t st = check_tensors(t, count, false);
-  if (st == MOE_OK) st = check_norm_call(t, count, norm, workspace, workspace_bytes);
-  if (st == MOE_OK) st = check_disjoint(t, count, false, norm, true, workspace, moe_grad_norm_workspace_size(t, count));
+  if (st != MOE_OK) return st;
+  const size_t need = parts_bytes(t, count);
+  st = check_norm_call(norm, workspace, workspace_bytes, need);
+  if (st == MOE_OK) st = check_disjoint(t, count, false, norm, true, workspace, need);
   if (st != MOE_OK) return st;
   int parts;
   st = run_squares(t, count, (double*)workspace, &parts, stream);
@@ -422,11 +440,10 @@ moe_status_t moe_clip_grads(const moe_tensor_t* t, int32_t count, float max_norm
     if (!norm) return MOE_ERR_INVALID_ARG;
     if (!aligned(norm, 4)) return MOE_ERR_MISALIGNED;
     workspace = nullptr;
-  } else if ((st = check_norm_call(t, count, norm, workspace, workspace_bytes)) != MOE_OK) {
-    return st;
   }
-  st = check_disjoint(t, count, true, norm, !norm_given, workspace,
-                      norm_given ? 0 : moe_grad_norm_workspace_size(t, count));
+  const size_t need = norm_given ? 0 : parts_bytes(t, count);
+  if (!norm_given && (st = check_norm_call(norm, workspace, workspace_bytes, need)) != MOE_OK) return st;
+  st = check_disjoint(t, count, true, norm, !norm_given, workspace, need);
   if (st != MOE_OK) return st;
   int parts = 0;
   if (!norm_given) {
