@@ -420,11 +420,8 @@ constexpr size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
-// Few tokens take the matrix-vector kernel, by the rule of the products: it does not wait for a tile's
-// whole reduction (2 tokens against 366 x 3400 38.6 us by tiles, 9.4 so; 20 against 442 x 3792 42 and 15).
-static bool few_logits(int64_t rows, int columns) { return takes_matrix_vector(rows, 1, columns); }
 static int loss_panels(int64_t rows, int V) {
-  const int w = few_logits(rows, V) ? kSkinnyColumns : TB;
+  const int w = takes_matrix_vector_logits(rows, V) ? kSkinnyColumns : TB;
   return (V + w - 1) / w;
 }
 
@@ -453,7 +450,7 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s) {
   t.a = (const char*)a.x;
   t.b = (const char*)a.w;
   t.npan = panels;
-  const bool few = few_logits(a.rows, a.V);
+  const bool few = takes_matrix_vector_logits(a.rows, a.V);
   const hipError_t e = few ? launch_loss_skinny(t.g, a.x, a.w, tokens, false, s)
                            : launch_rows(lc, k_loss_logits<true>, k_loss_logits<false>, t, LseEpi{tokens, a.rows});
   if (e != hipSuccess) return e;
@@ -525,7 +522,7 @@ hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
     hipError_t e = hipSuccess;
     if (a.rows > 0) {
       tokens.v0 = (int)v0;
-      e = few_logits(a.rows, n) ? launch_loss_skinny(t.g, a.x, w, tokens, true, s)
+      e = takes_matrix_vector_logits(a.rows, n) ? launch_loss_skinny(t.g, a.x, w, tokens, true, s)
                                 : launch_rows(lc, k_loss_grad<true>, k_loss_grad<false>, t, GradEpi{tokens});
       if (e != hipSuccess) return e;
     }

@@ -48,4 +48,20 @@ inline bool quantizes_inside(int64_t rows, int64_t x_rows, int E, int N, int K) 
          rows <= (int64_t)kInsideRows * E;
 }
 
+// Logits of tokens against a vocabulary, and their gradients: the matrix-vector
+// kernel takes 64 tokens and 16 columns a workgroup, so that small ones do not
+// wait for a tile's whole reduction (0.6 us a step of 64 elements for up to 64
+// tokens, 1 us for more, and 10), while it reads tokens and weights from the caches
+// many times over.  Both sides, us (tiles / matrix-vector), rows of 128, 512, 2048
+// and 4096 elements: 1 token, 1000 columns 9.0 / 10.4, 10.9 / 9.2, 22.6 / 9.7 and
+// 43.5 / 13.4; 64 tokens, 4000 columns 9.7 / 11.1, 13.8 / 12.6, 26.6 / 19.0 and 49 /
+// 29; 400 tokens, 1000 columns 15.0 / 12.3, 20.5 / 13.9, 41 / 28 and 72 / 49; 200
+// tokens, 4000 columns (1000 workgroups) 14.9 / 18.7, 20.2 / 22.5, 41 / 44 and 71 /
+// 77; 1000 tokens, 1000 columns 16.7 / 19.3, 21.9 / 23.0, 43 / 52 and 73 / 91; 16
+// tokens, 16000 columns 10.1 / 13.3, 12.1 / 15.6, 29.5 / 26.7 and 52 / 44.
+constexpr int64_t kSkinnyLogitGroups = 700;
+inline bool takes_matrix_vector_logits(int64_t rows, int64_t columns) {
+  return (rows + 63) / 64 * ((columns + 15) / 16) <= kSkinnyLogitGroups;
+}
+
 }  // namespace moe

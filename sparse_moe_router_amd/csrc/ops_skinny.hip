@@ -252,7 +252,11 @@ __global__ __launch_bounds__(64 * SW) void k_op_skinny(SkinnyArgs p) {
   const int n0 = blockIdx.x * (MODE == GATED_UNIT ? SN / 2 : SN);
   int e = blockIdx.y;
   Range range;
-  if (p.by_row) {
+  if constexpr (MODE == LOGITS || MODE == LOGIT_GRADS) {
+    // 64 tokens a workgroup row
+    e = 0;
+    range = limited(g, (int64_t)blockIdx.y * 64, (int64_t)blockIdx.y * 64 + 64);
+  } else if (p.by_row) {
     // the expert of row blockIdx.y, taken by the workgroup of its first row; of up to 256 experts all
     // offsets are on their way at a time, and the expert's own are among them
     const int64_t row = blockIdx.y;
@@ -320,7 +324,7 @@ hipError_t launch_loss_skinny(const Groups& g, const void* x, const void* w, con
   a.x = (const char*)x;
   a.w = (const char*)w;
   a.loss = loss;
-  const dim3 grid((unsigned)((g.N + SN - 1) / SN), 1);
+  const dim3 grid((unsigned)((g.N + SN - 1) / SN), (unsigned)((g.rows + 63) / 64));
   const Launch lc{s, nullptr, nullptr};
   return grad ? launch(lc, k_op_skinny<false, false, LOGIT_GRADS>, grid, dim3(64 * SW), a)
               : launch(lc, k_op_skinny<false, false, LOGITS>, grid, dim3(64 * SW), a);

@@ -10,7 +10,9 @@ from sparse_moe_router_amd import ops
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
 SHAPES = [(1, 1, 8), (1, 300, 64), (3, 7, 16), (64, 257, 72), (65, 1000, 136), (129, 4099, 64), (200, 255, 264),
-          (300, 513, 128), (257, 2049, 1032), (5, 70001, 16), (3001, 300, 264), (700, 4099, 16)]
+          (300, 513, 128), (257, 2049, 1032), (5, 70001, 16), (3001, 300, 264), (700, 4099, 16),
+          # by tiles of every height
+          (1, 11500, 16), (60, 11300, 8), (100, 6001, 24), (180, 4099, 72), (300, 2500, 40)]
 
 
 def inputs(T, V, H, scale=2.0, seed=0):
