@@ -274,7 +274,8 @@ moe_status_t moe_combine_grad(const moe_combine_t* d, moe_mat_t d_out, moe_mat_t
 
 /* ------------------------------------------------------------ clipping */
 
-/* One of many gradients: n elements in a row, aligned as their type only. */
+/* One of many gradients: n elements in a row, aligned as their type only; at most 2^40
+ * elements in all tensors of a call. */
 typedef struct {
   const void* in;
   void* out;              /* moe_clip_grads only; in place: out == in of the same type */
@@ -327,7 +328,8 @@ moe_status_t moe_cross_entropy(const moe_loss_t* d, const void* x, const void* w
  * gave it, d_loss fp32 [rows]; dx bf16 or fp32 [rows][ld] or not given, dw bf16 or
  * fp32 [V][H] or NULL.  The vocabulary goes by in pieces; the workspace
  * (moe_cross_entropy_grad_workspace_size bytes) holds one piece's dz, the sums of
- * dx and r. */
+ * dx and r.  The fp32 sums of dx repeat bit for bit for calls that ask for the same
+ * of the two gradients; without dw their order may be another. */
 size_t moe_cross_entropy_grad_workspace_size(const moe_loss_t* d);
 moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, const void* x, const void* w,
                                     const int64_t* target, const float* lse, moe_mat_t dx, moe_dtype_t dx_type, void* dw,

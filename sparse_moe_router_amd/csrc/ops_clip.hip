@@ -3,7 +3,8 @@
 //   norm = sqrt(sum over all tensors of g^2),  out = g min(1, max_norm / (norm + eps))
 // Bound by HBM: one pass reads all gradients and leaves a sum a workgroup, the
 // next one adds those in a fixed order (every workgroup for itself: a launch of
-// its own between the two would cost more) and scales.  Sums are of 64 bits: a
+// its own between the two costs more while there are few, 1000 tensors of 65536
+// elements 144 against 149 us; 4000 of them 662 against 543) and scales.  Sums are of 64 bits: a
 // product and an addition of doubles for each element stay below the time of
 // its bytes, and no size of a gradient overflows or vanishes in them.
 //
@@ -149,6 +150,7 @@ __global__ __launch_bounds__(CT) void k_squares(GradTable g, double* part) {
 
 __device__ __forceinline__ double join(const double* part, int parts, double* lds) {
   double s = 0.0;
+#pragma unroll 8
   for (int i = threadIdx.x; i < parts; i += CT) s += part[i];
   return block_sum(s, lds);
 }

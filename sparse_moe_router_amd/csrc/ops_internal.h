@@ -132,6 +132,7 @@ hipError_t launch_combine_grad(const CombineArgs& a, hipStream_t s);
 // Tensors of one launch over many gradients, cut into pieces; as kernel arguments (below 4 KB).
 constexpr int kClipTensors = 120;
 constexpr int kClipGroups = 2048;  // workgroups of a launch at most
+constexpr int kClipParts = 2 * kClipGroups;  // sums of workgroups that each workgroup of the scaling adds itself
 struct GradTable {
   const void* in[kClipTensors];
   void* out[kClipTensors];
@@ -191,7 +192,8 @@ struct LossPlan {
   int splits;  // parts of the reduction of dw
   size_t d_bytes, part_bytes, x_bytes, dw_bytes, bytes;
 };
-LossPlan loss_plan(int64_t rows, int V, int H);
+// Without dw there are more slices, so the plan without it needs at least as large a workspace.
+LossPlan loss_plan(int64_t rows, int V, int H, bool with_dw);
 size_t loss_workspace(int64_t rows, int V);
 hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s);
 hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s);

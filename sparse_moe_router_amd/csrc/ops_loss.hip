@@ -460,19 +460,22 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s) {
                 dim3(256), tokens, a.rows, panels, a.loss, a.lse_out);
 }
 
-LossPlan loss_plan(int64_t rows, int V, int H) {
+LossPlan loss_plan(int64_t rows, int V, int H, bool with_dw) {
   LossPlan p;
   const int64_t all = (V + TB - 1) / TB * (int64_t)TB, most = kLossPieceBytes / 2 / (rows < 1 ? 1 : rows) / TB * TB;
   p.piece = (int)(most >= all ? all : most < kLossPieceColumns ? (kLossPieceColumns < all ? kLossPieceColumns : all) : most);
   const int first = p.piece < V ? p.piece : V;  // columns of the first piece
-  const int64_t tiles = (rows + TB - 1) / TB * ((H + TB - 1) / TB);
-  // slices: the fewest that fill the chip's 256 workgroups best, of at least 512 columns each
-  p.slices = 1;
-  double best = 1e30;
-  for (int n = 1; n <= 32 && (n == 1 || first / n >= 512); ++n) {
-    const double waves = (double)((tiles * n + 255) / 256) / n + 0.01 * n;
-    if (waves < best) best = waves, p.slices = n;
-  }
+  const int64_t tiles = (rows < 1 ? 1 : (rows + TB - 1) / TB) * ((H + TB - 1) / TB);
+  // Slices: as many as fill half of the chip's 256 workgroups (dw's tiles, of as much work in all, take the
+  // other half meanwhile), or without dw all of them; each writes and reads its sums once more.  Both
+  // gradients in us with 1, 2, 4, 8 and 16 slices: 200 tokens x 64000 columns of 2048 (8 tiles) 1171, 674,
+  // 430, 293, 276; 999 x 32003 of 1032 (20) 601, 372, 263, 255, 257; 999 x 32000 of 2048 (32) 666, 457, 369,
+  // 386, 421; 2000 x 32000 of 2048 (64) 863, 713, 706, 739, 796; 4096 x 65536 of 2048 (128) 2709, 2703, 2750,
+  // 2852, 3035; 6000 x 32000 of 2048 (192) 1993, 2259, 2378, 2495, 2745.  dx alone: 999 of 2048 623, 402,
+  // 289, 251, 279; 2000 of 2048 773, 557, 473, 496, 551; 4096 2217, 1862, 1896, 1998, 2179.
+  int64_t n = (with_dw ? 128 : 256) / tiles;
+  n = n < first / 512 ? n : first / 512;
+  p.slices = n < 1 ? 1 : n > 16 ? 16 : (int)n;
   p.slice = ((first + p.slices - 1) / p.slices + 63) / 64 * 64;
   p.slices = (first + p.slice - 1) / p.slice;  // none of the first piece's is empty
   // parts of dw: as many as fit the 256 workgroups, of at least four steps of 64 tokens
@@ -488,7 +491,7 @@ LossPlan loss_plan(int64_t rows, int V, int H) {
 }
 
 hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
-  const LossPlan plan = loss_plan(a.rows, a.V, a.H);
+  const LossPlan plan = loss_plan(a.rows, a.V, a.H, a.dw != nullptr);
   uint16_t* d = (uint16_t*)workspace;
   float* part = (float*)((char*)workspace + plan.d_bytes);
   uint16_t* x = (uint16_t*)((char*)part + plan.part_bytes);

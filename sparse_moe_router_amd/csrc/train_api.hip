@@ -78,11 +78,14 @@ CombineArgs combine_args(const moe_combine_t* d) {
 
 size_t type_size(moe_dtype_t t) { return t == MOE_DT_FP32 ? 4 : 2; }
 
+constexpr int64_t kMaxElements = (int64_t)1 << 40;  // of all tensors of a call
 moe_status_t check_tensors(const moe_tensor_t* t, int32_t count, bool outs) {
   if (count < 0 || (count > 0 && !t)) return MOE_ERR_INVALID_ARG;
+  int64_t elements = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].n < 0 || !check_type(t[i].in_type) || (outs && !check_type(t[i].out_type))) return MOE_ERR_INVALID_ARG;
-    if (t[i].n > ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (t[i].n > kMaxElements - elements) return MOE_ERR_UNSUPPORTED_SHAPE;
+    elements += t[i].n;
     if (t[i].n == 0) continue;
     if (!t[i].in || (outs && !t[i].out)) return MOE_ERR_INVALID_ARG;
     if (!aligned(t[i].in, type_size(t[i].in_type)) || (outs && !aligned(t[i].out, type_size(t[i].out_type))))
@@ -449,11 +452,16 @@ moe_status_t moe_clip_grads(const moe_tensor_t* t, int32_t count, float max_norm
   if (!norm_given) {
     st = run_squares(t, count, (double*)workspace, &parts, stream);
     if (st != MOE_OK) return st;
-    if (parts == 0) return status_of(launch_norm((const double*)workspace, 0, norm, stream));  // no elements
+  }
+  const double* part = (const double*)workspace;
+  if (!norm_given && (parts == 0 || parts > kClipParts)) {  // no elements, or more parts than each workgroup adds
+    st = status_of(launch_norm(part, parts, norm, stream));
+    if (st != MOE_OK || parts == 0) return st;
+    part = nullptr;
   }
   bool store = true;
   return each_table(t, count, true, [&](const GradTable& g) {
-    const hipError_t e = launch_clip(g, (const double*)workspace, parts, norm, max_norm, eps, store, stream);
+    const hipError_t e = launch_clip(g, part, parts, norm, max_norm, eps, store, stream);
     store = false;
     return status_of(e);
   });
@@ -486,7 +494,7 @@ moe_status_t moe_cross_entropy(const moe_loss_t* d, const void* x, const void* w
 }
 
 size_t moe_cross_entropy_grad_workspace_size(const moe_loss_t* d) {
-  return check_loss(d) == MOE_OK ? loss_plan(d->rows, d->V, d->H).bytes : 0;
+  return check_loss(d) == MOE_OK ? loss_plan(d->rows, d->V, d->H, false).bytes : 0;
 }
 
 moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, const void* x, const void* w,
@@ -502,7 +510,7 @@ moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, co
     return MOE_ERR_MISALIGNED;
   if (dx.data && (st = check_mat(dx, d->H)) != MOE_OK) return st;
   if (d->rows > 0 && (!x || !w || !target || !lse || !d_loss || !workspace)) return MOE_ERR_INVALID_ARG;
-  const size_t need = loss_plan(d->rows, d->V, d->H).bytes;
+  const size_t need = loss_plan(d->rows, d->V, d->H, false).bytes;
   if (d->rows > 0 && workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   Regions r;
   loss_regions(&r, d, x, w, target);

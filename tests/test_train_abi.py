@@ -282,3 +282,12 @@ def test_binding_refuses_cpu_tensors():
         ops.grad_norm([1.0])
     with pytest.raises(TypeError):
         ops.cross_entropy_grad(f(4), b(4, 64), b(9, 64), torch.zeros(4).long(), f(4), dx_dtype=torch.float16)
+
+
+def test_clipping_refuses_too_many_elements():
+    """2^40 elements in all: none of the sums over the tensors' pieces overflows."""
+    half = (at(0), at(0), 1 << 39, 0, 0)
+    size = ops.lib().moe_grad_norm_workspace_size
+    assert size(tensors(half, half), 2) > 0 and size(tensors(half, half, ONE), 3) == 0
+    assert gnorm(t=(half, half, ONE)) == SHAPE and clip(t=(half, half, ONE)) == SHAPE
+    assert clip(t=(half, half, ONE), given=1, wk=None, wkb=0) == SHAPE

@@ -157,3 +157,20 @@ def test_refuses():
             call()
     assert (t == 1).all()
     ops.grad_norm([t, t])  # reading twice is no overlap
+
+
+def test_more_sums_than_a_workgroup_adds():
+    """363 tensors of 400003 elements: three launches, 4700 sums, which one more launch adds up."""
+    n, each = 363, 400003
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dev = [torch.randn(each, generator=g, device="cuda").mul_(0.1 + i % 7).to(BF16) for i in range(n)]
+    want = math.sqrt(math.fsum(float((t.to(F8) ** 2).sum()) for t in dev))
+    rel = 1.001 * EPS32 + n * each * 2.0 ** -53
+    mine = [t.clone() for t in dev]
+    norm = ops.clip_grads(mine, 2.5)
+    assert abs(norm.item() - want) <= rel * want
+    assert torch.equal(norm, ops.grad_norm(dev))
+    c = 2.5 / (want + 1e-6)
+    for a, b in zip(mine, dev):
+        w = b.to(F8) * c
+        assert ((a.to(F8) - w).abs() <= (3.01 * EPS32 + eps_of(BF16)) * w.abs() + 1e-37).all()

@@ -180,3 +180,21 @@ def test_refuses():
             call()
     with pytest.warns(UserWarning, match="requires a gradient"):
         ops.cross_entropy(x.clone().requires_grad_(), w, t)
+
+
+@pytest.mark.parametrize("T,V,H,least", [(999, 9001, 520, 9), (300, 20001, 72, 16), (2100, 1300, 2056, 1)])
+def test_slices_of_the_rows_gradient(T, V, H, least):
+    """dx by another number of slices where dw is not asked for (its workspace holds those)."""
+    x, w, t = inputs(T, V, H)
+    assert ops.lib().moe_cross_entropy_grad_workspace_size(ops.MoeLoss(T, H, V, H, -100)) >= T * V * 2 + least * T * H * 4
+    dl = torch.rand(T, generator=torch.Generator().manual_seed(9)) - 0.2
+    c = [v.cuda() for v in (dl, x, w, t)]
+    (dx, tx), (dw, tw) = ((v.cpu() for v in p) for p in U.loss_grad_ref(*c))
+    lse = ops.cross_entropy(*c[1:])[1]
+    for g in (ops.cross_entropy_grad(*c, lse, dx_dtype=F32, dw_dtype=F32),
+              ops.cross_entropy_grad(*c, lse, dx_dtype=F32, dw_dtype=None),
+              ops.cross_entropy_grad(*c, lse, dx_dtype=None, dw_dtype=F32)):
+        if "x" in g:
+            close(g["x"], dx, tx + EPS32 * dx.abs(), "x")
+        if "w" in g:
+            close(g["w"], dw, tw + EPS32 * dw.abs(), "w")

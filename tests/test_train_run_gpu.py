@@ -206,13 +206,14 @@ def test_given_workspaces():
                            p["off"].data_ptr(), p["perm"].data_ptr())
     h, gu = ops.gated_matmul(x, p["gu"], p["off"], save=True, perm=p["perm"], top_k=2)
     lse = ops.cross_entropy(x, w, t)[1]
+    tensors = (ops.MoeTensor * 2)(*(ops.MoeTensor(v.data_ptr(), None, v.numel(), 0, 0) for v in (w, x)))
     calls = [(lib.moe_cross_entropy_workspace_size(d), lambda **k: ops.cross_entropy(x, w, t, **k)),
              (lib.moe_cross_entropy_grad_workspace_size(d),
               lambda **k: ops.cross_entropy_grad(p["d_loss"], x, w, t, lse, **k).values()),
              (lib.moe_feed_forward_grad_workspace_size(f),
               lambda **k: ops.feed_forward_grad(p["dy"], x, p["gu"], p["down"], gu, p["off"], perm=p["perm"], top_k=2,
                                                 **k).values()),
-             (256, lambda **k: [ops.grad_norm([w, x], **k)])]
+             (lib.moe_grad_norm_workspace_size(tensors, 2), lambda **k: [ops.grad_norm([w, x], **k)])]
     for need, call in calls:
         assert need > 0
         want = list(call())
