@@ -328,8 +328,7 @@ moe_status_t moe_cross_entropy(const moe_loss_t* d, const void* x, const void* w
  * gave it, d_loss fp32 [rows]; dx bf16 or fp32 [rows][ld] or not given, dw bf16 or
  * fp32 [V][H] or NULL.  The vocabulary goes by in pieces; the workspace
  * (moe_cross_entropy_grad_workspace_size bytes) holds one piece's dz, the sums of
- * dx and r.  The fp32 sums of dx repeat bit for bit for calls that ask for the same
- * of the two gradients; without dw their order may be another. */
+ * dx and r.  Either gradient is the same, bit for bit, with and without the other. */
 size_t moe_cross_entropy_grad_workspace_size(const moe_loss_t* d);
 moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, const void* x, const void* w,
                                     const int64_t* target, const float* lse, moe_mat_t dx, moe_dtype_t dx_type, void* dw,

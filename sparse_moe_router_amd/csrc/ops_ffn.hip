@@ -49,6 +49,8 @@ Groups dx_groups(const FfnArgs& a) {
 }
 int64_t dx_units(const FfnArgs& a) { return row_tile_units(a.g, (a.g.K + TB - 1) / TB); }
 
+int64_t tiles_of(int64_t rows, int64_t columns) { return (rows + TB - 1) / TB * ((columns + TB - 1) / TB); }
+
 TileArgs weight_tiles(const Groups& g, const void* dy, const void* x, void* out, bool fp32, int splits) {
   TileArgs t{};
   t.g = g;
@@ -64,14 +66,22 @@ TileArgs weight_tiles(const Groups& g, const void* dy, const void* x, void* out,
 
 }  // namespace
 
-// Parts: as many as the 256 workgroups that run at a time hold, of at least four steps of 64 rows of a
-// group of average size.
+// Parts of the weight gradients: those with which the launch takes least (launch_steps; a group of average
+// size), of at least four steps of 64 rows.  Blocks of K = H, I and rows over E experts in us, by parts:
+// 1024, 512, 4096 over 1: 1 part 121, 4 84, 10 97; 2048, 1024, 4096 over 1: 1 148, 2 170, 4 161; 1024, 512,
+// 8192 over 4: 1 92, 2 115, 4 114; 1024, 512, 16384 over 1: 1 338, 4 157, 8 139, 16 171.
 int ffn_splits(const FfnArgs& a) {
-  const int64_t units = wgrad_units(a.g, 1) + wgrad_units(down_groups(a), 1);
-  const int64_t most = a.g.rows / (256 * (int64_t)a.g.E);
-  int64_t n = kChainGroups / units;
-  n = n < most ? n : most;
-  return n > 1 ? (int)n : 1;
+  const int64_t E = a.g.E, most = a.g.rows / (256 * E);
+  const int64_t units = E * tiles_of(a.g.N, a.g.K) + E * tiles_of(a.H, a.I), dx = tiles_of(a.g.rows, a.g.K);
+  const int64_t size = E * ((int64_t)a.g.N * a.g.K + (int64_t)a.H * a.I) * 4;
+  int best = 1;
+  int64_t least = 0;
+  for (int n = 1; n <= (most > 1 ? most : 1) && (n == 1 || n * units <= kMostTiles); n = next_parts(n)) {
+    const int64_t t = launch_steps(dx, a.g.N / 64 + kTileSteps, units * n, a.g.rows / (64 * E * n) + kTileSteps) +
+                      (n > 1 ? kLaunchSteps + 2 * n * size / kStepBytes : 0);
+    if (n == 1 || t < least) best = n, least = t;
+  }
+  return best;
 }
 size_t ffn_split_bytes(const FfnArgs& a) {
   const int n = ffn_splits(a);
@@ -98,12 +108,11 @@ hipError_t launch_ffn_products(const FfnArgs& a, float* part, hipStream_t s) {
   f.gu_units = (int)wgrad_units(a.g, n);
   const dim3 grid((unsigned)(f.dx_units + f.gu_units + wgrad_units(f.down.g, n))), block(512);
   const Launch lc{s, nullptr, nullptr};
-  hipError_t e = !a.g.perm             ? launch(lc, k_ffn_products<GX_ROWS>, grid, block, f)
-                 : rows_far(a.g, 2) ? launch(lc, k_ffn_products<GX_FAR>, grid, block, f)
-                                       : launch(lc, k_ffn_products<GX_INDEX>, grid, block, f);
+  const hipError_t e = !a.g.perm          ? launch(lc, k_ffn_products<GX_ROWS>, grid, block, f)
+                       : rows_far(a.g, 2) ? launch(lc, k_ffn_products<GX_FAR>, grid, block, f)
+                                          : launch(lc, k_ffn_products<GX_INDEX>, grid, block, f);
   if (e != hipSuccess || n == 1) return e;
-  e = launch_sum_parts(part, n, gu_size, nullptr, a.dw_gate_up, a.dw32, s);
-  return e != hipSuccess ? e : launch_sum_parts(down_part, n, down_size, nullptr, a.dw_down, a.dw32, s);
+  return launch_sum_parts(n, SumOf{part, gu_size, a.dw_gate_up}, SumOf{down_part, down_size, a.dw_down}, nullptr, a.dw32, s);
 }
 
 }  // namespace moe

@@ -192,8 +192,7 @@ struct LossPlan {
   int splits;  // parts of the reduction of dw
   size_t d_bytes, part_bytes, x_bytes, dw_bytes, bytes;
 };
-// Without dw there are more slices, so the plan without it needs at least as large a workspace.
-LossPlan loss_plan(int64_t rows, int V, int H, bool with_dw);
+LossPlan loss_plan(int64_t rows, int V, int H);
 size_t loss_workspace(int64_t rows, int V);
 hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s);
 hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s);

@@ -460,28 +460,40 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s) {
                 dim3(256), tokens, a.rows, panels, a.loss, a.lse_out);
 }
 
-LossPlan loss_plan(int64_t rows, int V, int H, bool with_dw) {
+LossPlan loss_plan(int64_t rows, int V, int H) {
   LossPlan p;
   const int64_t all = (V + TB - 1) / TB * (int64_t)TB, most = kLossPieceBytes / 2 / (rows < 1 ? 1 : rows) / TB * TB;
   p.piece = (int)(most >= all ? all : most < kLossPieceColumns ? (kLossPieceColumns < all ? kLossPieceColumns : all) : most);
   const int first = p.piece < V ? p.piece : V;  // columns of the first piece
   const int64_t tiles = (rows < 1 ? 1 : (rows + TB - 1) / TB) * ((H + TB - 1) / TB);
-  // Slices: as many as fill half of the chip's 256 workgroups (dw's tiles, of as much work in all, take the
-  // other half meanwhile), or without dw all of them; each writes and reads its sums once more.  Both
-  // gradients in us with 1, 2, 4, 8 and 16 slices: 200 tokens x 64000 columns of 2048 (8 tiles) 1171, 674,
-  // 430, 293, 276; 999 x 32003 of 1032 (20) 601, 372, 263, 255, 257; 999 x 32000 of 2048 (32) 666, 457, 369,
-  // 386, 421; 2000 x 32000 of 2048 (64) 863, 713, 706, 739, 796; 4096 x 65536 of 2048 (128) 2709, 2703, 2750,
-  // 2852, 3035; 6000 x 32000 of 2048 (192) 1993, 2259, 2378, 2495, 2745.  dx alone: 999 of 2048 623, 402,
-  // 289, 251, 279; 2000 of 2048 773, 557, 473, 496, 551; 4096 2217, 1862, 1896, 1998, 2179.
-  int64_t n = (with_dw ? 128 : 256) / tiles;
-  n = n < first / 512 ? n : first / 512;
-  p.slices = n < 1 ? 1 : n > 16 ? 16 : (int)n;
+  const int64_t pieces = (V + p.piece - 1) / p.piece;
+  const int64_t units = ((first + TB - 1) / TB) * (int64_t)((H + TB - 1) / TB);  // tiles of dw
+  const int64_t dx_size = rows * H * 4, dw_size = (int64_t)first * H * 4;
+  // Slices of dx and parts of dw: those with which a piece's launch takes least (launch_steps), three
+  // calls with dw to one without it (dx does not depend on whether dw is asked for).  Slices are written,
+  // from the second piece on read too, and added up at the end.  Both gradients / dx alone in us with 1, 2,
+  // 4, 8 and 16 slices: 200 tokens x 64000 columns of 2048 1171 / 1026, 674 / 570, 430 / 331, 293 / 216, 276
+  // / 169; 999 x 32000 of 2048 666 / 623, 457 / 402, 369 / 289, 386 / 251, 421 / 279; 2000 x 32000 of 2048
+  // 863 / 773, 713 / 557, 706 / 473, 739 / 496, 796 / 551; 4096 x 65536 of 2048 2709 / 2217, 2703 / 1862,
+  // 2750 / 1896, 2852 / 1998, 3035 / 2179; 6000 x 32000 of 2048 1993 / 1440, 2259 / 1693, 2378 / 1681, 2495
+  // / 1807, 2745 / 2050; with 1, 2, 4, 8 and 16 parts: 16000 x 1000 of 512 311, 189, 128, 100, 97.
+  p.slices = p.splits = 1;
+  int64_t least = 0;
+  for (int n = 1; n <= 32 && (n == 1 || (first / n >= 128 && tiles * n <= kMostTiles)); n = next_parts(n)) {
+    const int64_t steps = ((first + n - 1) / n + 63) / 64 + kTileSteps;
+    const bool direct = n == 1 && pieces == 1;
+    const int64_t sums = direct ? 0 : (pieces == 1 ? 1 : 2) * n * dx_size / kStepBytes;
+    const int64_t alone = pieces * (launch_steps(tiles * n, steps, 0, 0) + sums) +
+                          4 * (direct ? 0 : kLaunchSteps + n * dx_size / kStepBytes);
+    for (int m = 1; m == 1 || (m <= rows / 256 && units * m <= kMostTiles); m = next_parts(m)) {
+      const int64_t both = launch_steps(tiles * n, steps, units * m, rows / (64 * m) + kTileSteps) + sums +
+                           (m > 1 ? kLaunchSteps + 2 * m * dw_size / kStepBytes : 0);
+      const int64_t t = alone + 3 * pieces * both;
+      if ((n == 1 && m == 1) || t < least) p.slices = n, p.splits = m, least = t;
+    }
+  }
   p.slice = ((first + p.slices - 1) / p.slices + 63) / 64 * 64;
   p.slices = (first + p.slice - 1) / p.slice;  // none of the first piece's is empty
-  // parts of dw: as many as fit the 256 workgroups, of at least four steps of 64 tokens
-  const int64_t units = ((first + TB - 1) / TB) * (int64_t)((H + TB - 1) / TB), parts = kChainGroups / units;
-  p.splits = (int)(parts < rows / 256 ? parts : rows / 256);
-  if (p.splits < 1) p.splits = 1;
   p.d_bytes = align256((size_t)rows * p.piece * 2);
   p.part_bytes = align256((size_t)p.slices * rows * H * 4);
   p.x_bytes = align256((size_t)rows * H * 2);
@@ -491,7 +503,7 @@ LossPlan loss_plan(int64_t rows, int V, int H, bool with_dw) {
 }
 
 hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
-  const LossPlan plan = loss_plan(a.rows, a.V, a.H, a.dw != nullptr);
+  const LossPlan plan = loss_plan(a.rows, a.V, a.H);
   uint16_t* d = (uint16_t*)workspace;
   float* part = (float*)((char*)workspace + plan.d_bytes);
   uint16_t* x = (uint16_t*)((char*)part + plan.part_bytes);
@@ -554,7 +566,7 @@ hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
     e = launch(lc, plan.splits > 1 || a.rows == 0 ? k_loss_products<StoreEpi> : k_loss_products<ScaledEpi>,
                dim3((unsigned)units), dim3(512), f);
     if (e == hipSuccess && a.dw && plan.splits > 1)
-      e = launch_sum_parts(dw_part, plan.splits, (int64_t)n * a.H, most, dw, a.dw32, s);
+      e = launch_sum_parts(plan.splits, SumOf{dw_part, (int64_t)n * a.H, dw}, SumOf{}, most, a.dw32, s);
     if (e != hipSuccess) return e;
   }
   if (!a.dx || a.rows == 0 || direct) return hipSuccess;

@@ -494,7 +494,7 @@ moe_status_t moe_cross_entropy(const moe_loss_t* d, const void* x, const void* w
 }
 
 size_t moe_cross_entropy_grad_workspace_size(const moe_loss_t* d) {
-  return check_loss(d) == MOE_OK ? loss_plan(d->rows, d->V, d->H, false).bytes : 0;
+  return check_loss(d) == MOE_OK ? loss_plan(d->rows, d->V, d->H).bytes : 0;
 }
 
 moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, const void* x, const void* w,
@@ -510,7 +510,7 @@ moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, co
     return MOE_ERR_MISALIGNED;
   if (dx.data && (st = check_mat(dx, d->H)) != MOE_OK) return st;
   if (d->rows > 0 && (!x || !w || !target || !lse || !d_loss || !workspace)) return MOE_ERR_INVALID_ARG;
-  const size_t need = loss_plan(d->rows, d->V, d->H, false).bytes;
+  const size_t need = loss_plan(d->rows, d->V, d->H).bytes;
   if (d->rows > 0 && workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   Regions r;
   loss_regions(&r, d, x, w, target);

@@ -184,7 +184,7 @@ def test_refuses():
 
 @pytest.mark.parametrize("T,V,H,least", [(999, 9001, 520, 9), (300, 20001, 72, 16), (2100, 1300, 2056, 1)])
 def test_slices_of_the_rows_gradient(T, V, H, least):
-    """dx by another number of slices where dw is not asked for (its workspace holds those)."""
+    """Few and many slices of dx (the workspace holds them), with and without dw."""
     x, w, t = inputs(T, V, H)
     assert ops.lib().moe_cross_entropy_grad_workspace_size(ops.MoeLoss(T, H, V, H, -100)) >= T * V * 2 + least * T * H * 4
     dl = torch.rand(T, generator=torch.Generator().manual_seed(9)) - 0.2
