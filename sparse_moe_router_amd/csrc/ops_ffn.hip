@@ -47,7 +47,13 @@ Groups dx_groups(const FfnArgs& a) {
   g.perm = nullptr;
   return g;
 }
-int64_t dx_units(const FfnArgs& a) { return row_tile_units(a.g, (a.g.K + TB - 1) / TB); }
+// dx's tiles are low ones where the weight gradients' leave them the room.
+int64_t weight_units(const FfnArgs& a, int parts) { return wgrad_units(a.g, parts) + wgrad_units(down_groups(a), parts); }
+int dx_room(const FfnArgs& a, int parts) {
+  const int64_t weights = weight_units(a, parts);
+  return weights < kChainGroups ? (int)(kChainGroups - weights) : 0;
+}
+int64_t dx_units(const FfnArgs& a, int parts) { return row_tile_units(a.g, (a.g.K + TB - 1) / TB, dx_room(a, parts)); }
 
 int64_t tiles_of(int64_t rows, int64_t columns) { return (rows + TB - 1) / TB * ((columns + TB - 1) / TB); }
 
@@ -89,7 +95,7 @@ size_t ffn_split_bytes(const FfnArgs& a) {
 }
 int64_t ffn_units(const FfnArgs& a) {
   const int n = ffn_splits(a);
-  return dx_units(a) + wgrad_units(a.g, n) + wgrad_units(down_groups(a), n);
+  return dx_units(a, n) + weight_units(a, n);
 }
 
 hipError_t launch_ffn_products(const FfnArgs& a, float* part, hipStream_t s) {
@@ -102,9 +108,10 @@ hipError_t launch_ffn_products(const FfnArgs& a, float* part, hipStream_t s) {
   f.dx.b = (const char*)a.w_gate_up;
   f.dx.out = a.dx;
   f.dx.npan = (a.g.K + TB - 1) / TB;
+  f.dx.room = dx_room(a, n);
   f.gu = weight_tiles(gu_groups(a), a.d_pre, a.x, n > 1 ? part : a.dw_gate_up, n > 1 || a.dw32, n);
   f.down = weight_tiles(down_groups(a), a.dy, a.h, n > 1 ? down_part : a.dw_down, n > 1 || a.dw32, n);
-  f.dx_units = a.g.rows > 0 ? (int)dx_units(a) : 0;
+  f.dx_units = a.g.rows > 0 ? (int)dx_units(a, n) : 0;
   f.gu_units = (int)wgrad_units(a.g, n);
   const dim3 grid((unsigned)(f.dx_units + f.gu_units + wgrad_units(f.down.g, n))), block(512);
   const Launch lc{s, nullptr, nullptr};

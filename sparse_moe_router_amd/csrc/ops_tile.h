@@ -26,6 +26,7 @@ struct TileArgs {
   int fp32;
   int npan;    // tiles along the second output dimension
   int nrow;    // TN: tiles along n
+  int room;    // NT, NN: workgroups that the tiles may take
   int splits;           // TN: parts of the reduction (0 and 1: the whole)
   const float* factor;  // ScaledEpi
 };
@@ -119,16 +120,38 @@ struct RowTile {
   int once;  // the group's only tile, of weight rows in whole cache lines
 };
 
-// Workgroups of a launch whose tiles follow each other: one a compute unit.
+// Workgroups that run at a time, one a compute unit: those of a launch whose tiles follow each other.
 constexpr int kChainGroups = 256;
+
+// Heights of row tiles: where all of them run at a time, low ones, each of which takes less (a tile takes 0.6
+// us a step of up to 64 rows, 1 of 128 and 1.45 of 256; measured, us, tiles of 256 and these: 2000 x 2048 x
+// 2048 40 and 26, 256 x 8192 x 1024 25 and 16, 8192 x 512 x 4096 67 and 43, 400 x 1024 x 4096 66 and 34, by
+// rows of int8 42 and 28 for 1000 x 4096 x 4096; 1000 x 2048 against 1000 columns of logits 46 and 26).
+// `room`: the workgroups that the tiles of all panels may take.
+// Of one group: the number of its tiles.
+__host__ __device__ inline int64_t dense_tiles(int64_t rows, int64_t npan, int room) {
+  for (int h = 64; h < TB; h += 64) {
+    const int64_t n = (rows + h - 1) / h;
+    if (n * npan <= room) return n;
+  }
+  return (rows + TB - 1) / TB;
+}
+// Of several groups, whose sizes only the device knows: the exponent of 2 of the height.
+__host__ __device__ inline int64_t most_tiles(const Groups& g, int shift) {
+  return (g.rows >> shift) + (g.E < g.rows ? g.E : g.rows);
+}
+__host__ __device__ inline int tile_shift(const Groups& g, int64_t npan, int room) {
+  return most_tiles(g, 6) * npan <= room ? 6 : most_tiles(g, 7) * npan <= room ? 7 : 8;
+}
+static_assert(TB == 1 << 8, "tile_shift");
 
 // One group: the units (tile, panel) are cut into eight equal runs, one for
 // each XCD, and within a run into blocks of four tiles, panel by panel: the 32
 // workgroups that an XCD runs at a time then read about as many tiles' rows as
 // panels' weights (int8 4096 x 8192 x 4096: 126 -> 119 us).
-__device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int64_t local, int npan, bool aligned) {
+__device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int64_t local, int npan, bool aligned, int room) {
   constexpr int SG = 4;
-  const int64_t total = (g.rows + TB - 1) / TB;
+  const int64_t total = dense_tiles(g.rows, npan, room);
   // Where all units run at a time, the tiles share the rows evenly, in whole blocks of 32: the tallest one
   // takes the time of the launch (257 rows against 32003 columns of 2048: 256 + 1 rows 56 us, 160 + 97 50).
   const int height_rows = total * npan <= kChainGroups ? (int)((g.rows + 32 * total - 1) / (32 * total)) * 32 : TB;
@@ -149,7 +172,7 @@ __device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int
 // Against tiles dealt to the XCDs one by one, and against one run for each XCD
 // in group order: 8192 tokens x 2 over 16 experts 122, 136 and 148 us; 4096 x
 // 8 over 256 experts 241, 304, 241; 2501 x 4 over 60 skewed ones 51, 52, 60.
-// With fewer than 64 tiles single panels are dealt out.
+// With fewer than 64 tiles single panels are dealt out.  Low tiles are one class.
 // Lane l scans the groups [l * per, (l + 1) * per); every wave does the same scan.
 constexpr int kDealTiles = 64;
 // The ranges of groups e .. e + 3, empty from group `end` or E on; their loads are in flight together.
@@ -162,8 +185,9 @@ __device__ __forceinline__ void four_ranges(const Groups& g, int e, int end, Ran
   for (int u = 0; u < 4; ++u) r[u] = limited(g, v[u], v[u + 1]);
 }
 __device__ __forceinline__ int tile_class(int rest) { return rest > 192 ? 0 : rest > 64 ? 1 : 2; }
-__device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan, bool aligned) {
-  if (!g.offsets) return find_tile_dense(g, xcd, local, npan, aligned);
+__device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan, bool aligned, int room) {
+  if (!g.offsets) return find_tile_dense(g, xcd, local, npan, aligned, room);
+  const int shift = tile_shift(g, npan, room), low = (1 << shift) - 1;
   const int lane = threadIdx.x & 63, per = (g.E + 63) / 64;
   // tiles of this lane's groups in each class: bits 0..31, 32..47, 48..63
   uint64_t mine = 0;
@@ -173,8 +197,8 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t c = (uint32_t)r[u].size(), rest = c % TB;
-      mine += c / TB;
-      if (rest > 0) mine += (uint64_t)1 << (tile_class(rest) == 0 ? 0 : 16 + 16 * tile_class(rest));
+      mine += shift < 8 ? (c + low) >> shift : c / TB;
+      if (shift == 8 && rest > 0) mine += (uint64_t)1 << (tile_class(rest) == 0 ? 0 : 16 + 16 * tile_class(rest));
     }
   }
   uint64_t incl = mine;
@@ -210,21 +234,21 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
     cl = i < n0 ? 0 : i < n0 + n1 ? 1 : 2;
     i -= cl == 0 ? 0 : cl == 1 ? n0 : n0 + n1;
   }
-  const int shift = cl == 0 ? 0 : 16 + 16 * cl;
+  const int at = cl == 0 ? 0 : 16 + 16 * cl;
   const uint64_t mask = cl == 0 ? 0xFFFFFFFFu : 0xFFFFu;
-  const int src = __builtin_ctzll(__ballot((int64_t)((incl >> shift) & mask) > i));
-  i -= (int64_t)((__shfl(incl - mine, src, 64) >> shift) & mask);
+  const int src = __builtin_ctzll(__ballot((int64_t)((incl >> at) & mask) > i));
+  i -= (int64_t)((__shfl(incl - mine, src, 64) >> at) & mask);
   for (int j = 0; j < per; j += 4) {
     Range r[4];
     four_ranges(g, src * per + j, src * per + per, r);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t full = r[u].size() / TB;
-      const int rest = (int)(r[u].size() % TB);
-      const int64_t here = (cl == 0 ? full : 0) + (rest > 0 && tile_class(rest) == cl);
+      const int64_t size = r[u].size(), full = size >> shift;
+      const int rest = (int)(size & low);
+      const int64_t here = (cl == 0 ? full : 0) + (rest > 0 && (shift < 8 || tile_class(rest) == cl));
       if (i < here) {
         const int64_t k = cl == 0 ? i : full;  // the tile's place in its group
-        return RowTile{src * per + j + u, r[u].lo + k * TB, k < full ? TB : rest, panel, r[u].size() <= TB && aligned};
+        return RowTile{src * per + j + u, r[u].lo + (k << shift), k < full ? low + 1 : rest, panel, size <= low + 1 && aligned};
       }
       i -= here;
     }
@@ -798,7 +822,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, TileJob job, u32
 // rows again.
 template <OpKind KIND, bool I8, int GX, class EPI = StoreEpi>
 __device__ __forceinline__ void row_tile(const TileArgs& p, u32x4_t* lds, const EPI& epi = EPI{}) {
-  RowTile tl = find_tile(p.g, blockIdx.x & 7, blockIdx.x >> 3, p.npan, p.g.K * (I8 ? 1 : 2) % 128 == 0);
+  RowTile tl = find_tile(p.g, blockIdx.x & 7, blockIdx.x >> 3, p.npan, p.g.K * (I8 ? 1 : 2) % 128 == 0, p.room);
   // the same in every lane, which the compiler cannot see behind the scan
   tl = RowTile{__builtin_amdgcn_readfirstlane(tl.e), uniform64(tl.p0), __builtin_amdgcn_readfirstlane(tl.rows),
                __builtin_amdgcn_readfirstlane(tl.panel), __builtin_amdgcn_readfirstlane(tl.once)};
@@ -835,7 +859,7 @@ template <OpKind KIND, class EPI = StoreEpi>
 __device__ __forceinline__ void row_chain(const TileArgs& p, u32x4_t* lds, const EPI& epi = EPI{}) {
   int64_t local = blockIdx.x >> 3;
   auto take = [&](TileJob* t) __attribute__((always_inline)) {
-    const RowTile tl = find_tile_dense(p.g, blockIdx.x & 7, local, p.npan, false);
+    const RowTile tl = find_tile_dense(p.g, blockIdx.x & 7, local, p.npan, false, p.room);
     *t = TileJob{0, tl.p0, tl.rows, 0, 0, tl.panel};
     return tl.e >= 0;
   };
@@ -881,9 +905,11 @@ __device__ __forceinline__ void wgrad_tile(const TileArgs& args, int b, u32x4_t*
 }
 
 // Workgroups of a launch of row tiles with npan panels each.
-inline int64_t row_tile_units(const Groups& g, int64_t npan) {
-  const int64_t tiles = (g.rows + TB - 1) / TB + (g.offsets ? (g.E < g.rows ? g.E : g.rows) : 0);
-  return g.offsets && tiles >= kDealTiles ? ((tiles + 7) / 8 + 3) * 8 * npan : (tiles * npan + 7) / 8 * 8;
+inline int64_t row_tile_units(const Groups& g, int64_t npan, int room = kChainGroups) {
+  if (!g.offsets) return (dense_tiles(g.rows, npan, room) * npan + 7) / 8 * 8;
+  const int shift = tile_shift(g, npan, room);
+  const int64_t tiles = most_tiles(g, shift);
+  return tiles >= kDealTiles ? ((tiles + 7) / 8 + 3) * 8 * npan : (tiles * npan + 7) / 8 * 8;
 }
 // Gathered rows past the range of a buffer descriptor are fetched by 64-bit addresses.  So are they
 // where x has no row at all: every index then stands for zeros, which that form reads from kZero,
