@@ -11,6 +11,12 @@
 // gradient of h never leaves the registers; the tile's gate and up values are
 // fetched while the accumulators go through LDS, and the two gradients and h,
 // which the weight gradient of the next projection reads, leave together.
+//
+// Forward: 4096 tokens x 8 over 256 experts of 512 x 2048: 218 us, bound by the stream of the weights (1124
+// MB in and out at 5.2 TB/s; two kernels would write and read another 134 MB).  With the products kept, 2501
+// x 4 rows over 60 skewed experts of 1000 x 1416: 136 us for 407 MB; rows of 2832 bytes start off the cache
+// lines, which two steps then share (rows of 2816 bytes: 112).  Backward: 8192 x 2 rows over 16 experts of
+// 1024 x 2048: 112 to 130 us; 288 tiles are two rounds of 256 workgroups (matrix units busy 28% at 2.0 GHz).
 #include "ops_tile.h"
 
 namespace moe {

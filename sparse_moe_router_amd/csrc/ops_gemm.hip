@@ -28,6 +28,9 @@
 // of weights, tokens and results, 1158 MB), and weight gradients over short
 // groups by their results, which nothing overlaps with the next tile's loads
 // (the same rows: 395 us for 1.07 GB in bf16, 560 us for 2.15 GB in fp32).
+// Tiles of one group that follow each other in a workgroup overlap the two (4096 x
+// 16384, NT in us: K 256 76 -> 52, 1024 132 -> 120, 2048 224 -> 211); where all tiles
+// run at a time they are low ones (ops_tile.h).
 #include "ops_tile.h"
 
 namespace moe {
