@@ -8,9 +8,9 @@
 // tiles (few experts) are cut along their rows; the parts are added in a fixed
 // order by a second launch.
 //
-// 8192 x 2 rows over 16 experts of 1024 x 2048: 360 to 420 us = 0.82 to 0.95 PFLOP/s (matrix units busy 50% at
+// 8192 x 2 rows over 16 experts of 1024 x 2048: 352 to 429 us = 0.80 to 0.98 PFLOP/s (matrix units busy 50% at
 // 1.8 GHz: tiles of 16 and 32 steps, whose prologue and epilogue nothing overlaps).  701 x 4 rows over 64
-// skewed experts of 512 x 1032: 124 us, tiles of a few steps, each with up to 128 KB of results to store.
+// skewed experts of 512 x 1032: 126 us, tiles of a few steps, each with up to 128 KB of results to store.
 #include "ops_sum.h"
 #include "ops_tile.h"
 

@@ -16,7 +16,7 @@
 // MB in and out at 5.2 TB/s; two kernels would write and read another 134 MB).  With the products kept, 2501
 // x 4 rows over 60 skewed experts of 1000 x 1416: 136 us for 407 MB; rows of 2832 bytes start off the cache
 // lines, which two steps then share (rows of 2816 bytes: 112).  Backward: 8192 x 2 rows over 16 experts of
-// 1024 x 2048: 112 to 130 us; 288 tiles are two rounds of 256 workgroups (matrix units busy 28% at 2.0 GHz).
+// 1024 x 2048: 111 to 131 us; 288 tiles are two rounds of 256 workgroups (matrix units busy 28% at 2.0 GHz).
 #include "ops_tile.h"
 
 namespace moe {

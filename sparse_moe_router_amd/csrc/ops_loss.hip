@@ -20,8 +20,8 @@
 // share of that, exactly 1 for a mean, into the bf16 copy of x that it reads.
 //
 // 4096 tokens against 65536 x 2048: logits 900 to 946 us = 1.16 to 1.22 PFLOP/s (matrix units busy 69% at 1.6
-// GHz), their gradients 2 x 511 to 528 = 1.04 to 1.08 (58% at 1.7 GHz: each
-// tile has 128 KB to store), products 2 x 808 to 852 = 1.29 to 1.36 (74% at 1.7 GHz): power as much as the loop.
+// to 1.7 GHz), their gradients 2 x 511 to 528 = 1.04 to 1.08 (57% at 1.7 to 1.8 GHz: each
+// tile has 128 KB to store), products 2 x 808 to 852 = 1.29 to 1.36 (75% at 1.7 GHz): power as much as the loop.
 // 257 tokens against 32003 x 2048: 44 us, 131 MB of weights at 3 TB/s: the 32 steps of the one tile that a
 // workgroup has, with two stages in flight, not the bytes.
 #include "ops_loss.h"
