@@ -225,8 +225,8 @@ typedef struct {
  * dy bf16 [rows][ld_dy], x bf16 [x_rows][ldx], w_gate_up bf16 [E][2 I][K], w_down bf16
  * [E][H][I], gate_up bf16 [rows][ld] of 2 I columns as the forward call kept it, dx bf16
  * [rows][ld], dw_gate_up and dw_down in dw_type, of the weights' shapes.  workspace:
- * moe_feed_forward_grad_workspace_size bytes, which hold d_gate_up, h and, where few experts
- * have long groups, parts of the weight gradients. */
+ * moe_feed_forward_grad_workspace_size bytes, which hold d_gate_up, h (both bf16, or fp32 in
+ * calls of few rows) and, where few experts have long groups, parts of the weight gradients. */
 size_t moe_feed_forward_grad_workspace_size(const moe_feed_forward_t* d);
 moe_status_t moe_feed_forward_grad(const moe_feed_forward_t* d, const void* dy, const void* x, const void* w_gate_up,
                                    const void* w_down, moe_mat_t gate_up, moe_mat_t dx, void* dw_gate_up, void* dw_down,

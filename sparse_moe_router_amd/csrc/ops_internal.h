@@ -92,6 +92,9 @@ int ffn_splits(const FfnArgs& a);
 size_t ffn_split_bytes(const FfnArgs& a);
 int64_t ffn_units(const FfnArgs& a);
 hipError_t launch_ffn_products(const FfnArgs& a, float* part, hipStream_t s);
+// The whole backward pass for few rows, d [rows][2 I] and h [rows][I] in fp32.
+hipError_t launch_few_rows(const FfnArgs& a, const void* w_down, const void* pre, int64_t ldp, float* d, float* h,
+                           hipStream_t s);
 // dy W through the gate: d_pre and h of g.K features.
 hipError_t launch_gated_grad(const Groups& g, const void* dy, const void* w, const void* pre, int64_t ldp, void* d_pre,
                              int64_t ldd, void* h, int64_t ldh, hipStream_t s);

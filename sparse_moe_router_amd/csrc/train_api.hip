@@ -29,6 +29,7 @@ moe_status_t status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : hip_fai
 // A feed-forward block on checked shapes, and its workspace.
 struct Ffn {
   FfnArgs a;
+  bool few;  // kernels for few rows, which keep d and h in fp32
   size_t d_pre_bytes, h_bytes, bytes;
 };
 moe_status_t check_ffn(const moe_feed_forward_t* d, Ffn* f) {
@@ -49,9 +50,11 @@ moe_status_t check_ffn(const moe_feed_forward_t* d, Ffn* f) {
   f->a.ld_dpre = 2 * (int64_t)d->I;
   f->a.ld_h = d->I;
   if (op_tile_units(OP_NN, e.g) > kOpMaxUnits || ffn_units(f->a) > kOpMaxUnits) return MOE_ERR_UNSUPPORTED_SHAPE;
-  f->d_pre_bytes = ((size_t)d->rows * 2 * d->I * 2 + 255) & ~(size_t)255;
-  f->h_bytes = ((size_t)d->rows * d->I * 2 + 255) & ~(size_t)255;
-  f->bytes = f->d_pre_bytes + f->h_bytes + ffn_split_bytes(f->a);
+  f->few = takes_few_rows(d->rows, d->E, d->H, d->I, d->K);
+  const size_t size = f->few ? 4 : 2;
+  f->d_pre_bytes = ((size_t)d->rows * 2 * d->I * size + 255) & ~(size_t)255;
+  f->h_bytes = ((size_t)d->rows * d->I * size + 255) & ~(size_t)255;
+  f->bytes = f->d_pre_bytes + f->h_bytes + (f->few ? 0 : ffn_split_bytes(f->a));
   return MOE_OK;
 }
 
@@ -321,7 +324,7 @@ moe_status_t moe_feed_forward_grad(const moe_feed_forward_t* d, const void* dy, 
   // workspace: d_pre, h, parts of the weight gradients
   char* const d_pre = (char*)workspace;
   char* const h = d_pre + f.d_pre_bytes;
-  if (d->rows > 0) {
+  if (d->rows > 0 && !f.few) {
     Groups g = f.a.g;  // of the down projection
     g.N = d->H;
     g.K = d->I;
@@ -341,6 +344,7 @@ moe_status_t moe_feed_forward_grad(const moe_feed_forward_t* d, const void* dy, 
   a.dw_gate_up = dw_gate_up;
   a.dw_down = dw_down;
   a.dw32 = dw_type == MOE_DT_FP32;
+  if (f.few) return status_of(launch_few_rows(a, w_down, gate_up.data, gate_up.ld, (float*)d_pre, (float*)h, stream));
   return status_of(launch_ffn_products(a, (float*)(h + f.h_bytes), stream));
 }
 

@@ -20,11 +20,13 @@ def rules(tmp_path_factory):
         '#include "ops_paths.h"\n'
         'extern "C" int64_t steps(int64_t a, int64_t b, int64_t c, int64_t d) { return moe::launch_steps(a, b, c, d); }\n'
         'extern "C" int next(int n) { return moe::next_parts(n); }\n'
+        'extern "C" int few(int64_t r, int64_t e, int64_t h, int64_t i, int64_t k) { return moe::takes_few_rows(r, e, h, i, k); }\n'
         'extern "C" int logits(int64_t r, int64_t c) { return moe::takes_matrix_vector_logits(r, c); }\n')
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I",
                     os.path.join(ROOT, "sparse_moe_router_amd", "csrc"), str(d / "r.cpp"), "-o", str(d / "r.so")], check=True)
     lib = ctypes.CDLL(str(d / "r.so"))
     lib.steps.restype, lib.steps.argtypes = ctypes.c_int64, [ctypes.c_int64] * 4
+    lib.few.argtypes = [ctypes.c_int64] * 5
     lib.logits.argtypes = [ctypes.c_int64] * 2
     return lib
 
@@ -60,3 +62,11 @@ def test_logits_of_few_tokens_run_at_a_time(rules):
     for rows, columns, few in ((1, 16, 1), (64, 4096, 1), (64, 4097, 0), (65, 2048, 1), (65, 2049, 0), (16384, 16, 1),
                                (16385, 16, 0), (1 << 30, 1, 0), (1, 1 << 20, 0)):
         assert bool(rules.logits(rows, columns)) == bool(few), (rows, columns)
+
+
+def test_few_rows_of_small_blocks(rules):
+    """At most 32 rows, 2^28 weights read for them and as many gradients written."""
+    for rows, e, h, i, k, few in ((0, 1, 8, 8, 8, 0), (1, 1, 8, 8, 8, 1), (32, 1024, 8, 8, 8, 1), (33, 1, 8, 8, 8, 0),
+                                  (32, 1, 2048, 1344, 2048, 1), (32, 1, 2048, 1408, 2048, 0), (1, 42, 2048, 1024, 2048, 1),
+                                  (1, 43, 2048, 1024, 2048, 0), (1, 1, 1 << 20, 16384, 16384, 0)):
+        assert bool(rules.few(rows, e, h, i, k)) == bool(few), (rows, e, h, i, k)

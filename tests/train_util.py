@@ -34,8 +34,8 @@ def gated_ref(rows64, w, offsets):
     return (h, th + EPS16 * (h.abs() + th)), (pre, t + EPS16 * (pre.abs() + t))
 
 
-def gated_grad_ref(dy, w, gate_up, offsets):
-    """((d_gate_up, tol), (h, tol)); rows of no group NaN."""
+def gated_grad_raw(dy, w, gate_up, offsets):
+    """((d_gate_up, tol), (h, tol)) before their rounding to bf16; rows of no group NaN."""
     dh, t = grouped_ref(dy.to(F8), w.transpose(1, 2), offsets)
     I = dh.shape[1]
     g, u = gate_up[:, :I].to(F8), gate_up[:, I:].to(F8)
@@ -46,10 +46,33 @@ def gated_grad_ref(dy, w, gate_up, offsets):
                     t * (g * s).abs() + (dh.abs() + t) * (g * s).abs() * rz(g)], 1)
     far = (dh.abs() + t) * FLUSH
     td = td + torch.cat([far * u.abs() * (1 + g.abs()), far * g.abs()], 1)
-    d = torch.cat([dg, du], 1)
-    th = h.abs() * (rz(g) + EPS16 * 1.01) + (g * u).abs() * FLUSH
-    h = torch.where(torch.isnan(dh), dh, h)
-    return (d, td + EPS16 * (d.abs() + td)), (h, th)
+    th = h.abs() * rz(g) + (g * u).abs() * FLUSH
+    return (torch.cat([dg, du], 1), td), (torch.where(torch.isnan(dh), dh, h), th)
+
+
+def gated_grad_ref(dy, w, gate_up, offsets):
+    """((d_gate_up, tol), (h, tol)); rows of no group NaN."""
+    (d, td), (h, th) = gated_grad_raw(dy, w, gate_up, offsets)
+    return (d, td + EPS16 * (d.abs() + td)), (h, th + EPS16 * 1.01 * torch.nan_to_num(h).abs())
+
+
+def feed_forward_grad_raw(dy, x64, w_gate_up, w_down, gate_up, offsets):
+    """{name: (gradient, tol)} of a block before the results' rounding, nothing rounded between: products of fp32
+    values whose sums take 2 EPS32 a term; x64 the grouped rows of x.  Rows of no group NaN."""
+    (d, td), (h, th) = gated_grad_raw(dy, w_down, gate_up, offsets)
+    (E, I2, K), H = w_gate_up.shape, w_down.shape[1]
+    dx, tx = torch.full((len(dy), K), float("nan"), dtype=F8), torch.zeros(len(dy), K, dtype=F8)
+    gu, tgu, dn, tdn = (torch.zeros(s, dtype=F8) for s in ((E, I2, K), (E, I2, K), (E, H, I2 // 2), (E, H, I2 // 2)))
+    for e in range(E):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        n = r.stop - r.start
+        if n <= 0:
+            continue
+        w, dd, a, y = w_gate_up[e].to(F8), d[r].abs() + td[r], x64[r].abs(), dy[r].to(F8)
+        dx[r], tx[r] = d[r] @ w, td[r] @ w.abs() + 2 * EPS32 * I2 * (dd @ w.abs())
+        gu[e], tgu[e] = d[r].t() @ x64[r], td[r].t() @ a + 2 * EPS32 * n * (dd.t() @ a)
+        dn[e], tdn[e] = y.t() @ h[r], y.abs().t() @ (th[r] + 2 * EPS32 * n * (h[r].abs() + th[r]))
+    return {"x": (dx, tx), "w_gate_up": (gu, tgu), "w_down": (dn, tdn)}
 
 
 def invert_ref(perm, n, end):
