@@ -201,8 +201,14 @@ int64_t forward_rows(Call& c, PyObject* out, PyObject* perm, const Tensor& x) {
 }
 
 PyObject* wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
+// A tensor of the caller's has other values now: a graph of torch's differentiation that had saved it
+// refuses to use them.  (A tensor of the inference mode has no version.)
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 PyObject* result(PyObject* o, Tensor& own) {
   if (!given(o)) return wrap(std::move(own));
+  written(THPVariable_Unpack(o));
   Py_INCREF(o);
   return o;
 }
@@ -796,7 +802,12 @@ PyObject* clip_grads(PyObject*, Args a, Py_ssize_t n) {
     check(moe_clip_grads(v.data(), count_of(v), (float)max_norm, (float)eps, np ? np : (float*)norm.data_ptr(), np != nullptr,
                          wkp, have, c.stream),
           "moe_clip_grads");
-    return result(a[2], norm);
+    PyObject* const outs = given(a[4]) ? a[4] : a[0];
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(outs); ++i)
+      written(THPVariable_Unpack(PySequence_Fast_GET_ITEM(outs, i)));
+    if (!np) return wrap(norm);
+    Py_INCREF(a[2]);  // read only
+    return a[2];
   });
 }
 

@@ -14,7 +14,9 @@ not pass is allocated there, workspaces among it, so that calls on different
 streams and captured graphs never share one; tensors written on other streams
 must be ready on it.  Nothing is recorded for automatic differentiation: the
 gradients are calls of their own, and a tensor that requires a gradient where
-torch records them gives a warning.
+torch records them gives a warning.  A tensor of the caller's that a call writes
+(an ``out``, a list clipped in place) has a new version afterwards, so that a
+graph which had saved it refuses its new values.
 
 ``offsets`` (int32 [E+1]) and ``perm`` (int32 [rows]) are the group offsets and
 the permutation that :func:`sparse_moe_router_amd.route` reports.
