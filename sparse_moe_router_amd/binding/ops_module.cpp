@@ -74,14 +74,16 @@ struct Call {
     }
     if (t.dim() != dims)
       value_error(std::string(name) + " must have " + std::to_string(dims) + " dimension(s), got " + shape_of(t));
-    if (t.requires_grad() && c10::GradMode::is_enabled() && !warned) {
-      warned = true;
-      // at the line that calls ops.py
-      const std::string text = std::string(name) + " requires a gradient, which this call does not record: use its "
-                               "gradient call, from torch.no_grad() or a torch.autograd.Function";
-      if (PyErr_WarnEx(PyExc_UserWarning, text.c_str(), 3) != 0) throw PythonError{};
-    }
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+      warn(std::string(name) + " requires a gradient, which this call does not record: use its gradient call, from "
+                               "torch.no_grad() or a torch.autograd.Function");
     return t;
+  }
+  // once a call, at the line that calls ops.py, whose own frames there are `frames` of
+  void warn(const std::string& text, int frames = 2) {
+    if (warned) return;
+    warned = true;
+    if (PyErr_WarnEx(PyExc_UserWarning, text.c_str(), frames + 1) != 0) throw PythonError{};
   }
   // a contiguous tensor of exactly this shape; its address
   void* flat(PyObject* o, Types types, std::initializer_list<int64_t> shape, const char* name) {
@@ -733,6 +735,9 @@ const Tensor& gradient(Call& c, PyObject* o, const char* name, Py_ssize_t i) {
     type_error(std::string(name) + "[" + std::to_string(i) + "] must be BFloat16 or Float, got " +
                c10::toString(t.scalar_type()));
   if (!t.is_contiguous()) fail("must be contiguous");
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    c.warn(std::string(name) + "[" + std::to_string(i) + "] requires a gradient, which this call does not record: call it "
+           "from torch.no_grad()", 3);
   return t;
 }
 // The list's tensors; with outs (None: in place) as their results.

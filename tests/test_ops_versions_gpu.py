@@ -1,6 +1,9 @@
 """Tensors that the operators write into, as torch's automatic differentiation sees them: each has a new version
 afterwards, so that a graph which had saved one before refuses to use the new values as the old ones; those that
-are only read keep theirs."""
+are only read keep theirs.  A gradient in a list that requires a gradient itself gives the warning that other
+arguments give."""
+import warnings
+
 import pytest
 import torch
 
@@ -108,3 +111,18 @@ def test_refused_calls_leave_the_version():
     with pytest.raises(ops.MoeError):
         ops.clip_grads(g, -1.0)
     assert a._version == v and g[0]._version == 0
+
+
+def test_lists_warn_where_a_gradient_would_be_recorded():
+    p = torch.ones(8, device="cuda", requires_grad=True)
+    for call in (lambda: ops.grad_norm([p]), lambda: ops.clip_grads([p], 1.0, out=[torch.empty(8, device="cuda")])):
+        with pytest.warns(UserWarning, match="requires a gradient") as w:
+            call()
+        assert len(w) == 1 and w[0].filename == __file__
+        with torch.no_grad(), warnings.catch_warnings():
+            warnings.simplefilter("error")
+            call()
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(UserWarning):
+            ops.grad_norm([p])
