@@ -52,18 +52,18 @@ __global__ __launch_bounds__(512, 1) void k_op_rows_chain(TileArgs p) {
 template <int GX>
 __global__ __launch_bounds__(512, 1) void k_op_wgrad(TileArgs p) {
   __shared__ u32x4_t lds[10 * HU];
-  wgrad_tile<GX>(p, blockIdx.x, lds);
+  wgrad_tile<GX, StoreEpi, false>(p, blockIdx.x, lds);
 }
 // Of one matrix, whose units all take the same time: 32 workgroups of an XCD take its units in turn.
 __global__ __launch_bounds__(512, 1) void k_op_wgrad_chain(TileArgs p) {
   __shared__ u32x4_t lds[10 * HU];
   int unit = blockIdx.x;
   TileJob t;
-  if (wgrad_unit(p, unit, &t) < 0) return;
+  if (wgrad_unit<false>(p, unit, &t) < 0) return;
   tile_product<OP_TN, false, 2, 2, GX_ROWS, false>(p, t, lds, nullptr, StoreEpi{},
                                                    chain_next([&](TileJob& t) __attribute__((always_inline)) {
                                                      unit += kChainGroups;
-                                                     return wgrad_unit(p, unit, &t) >= 0;
+                                                     return wgrad_unit<false>(p, unit, &t) >= 0;
                                                    }));
 }
 
