@@ -112,7 +112,7 @@ hipError_t launch_ffn_products(const FfnArgs& a, float* part, hipStream_t s) {
   f.dx.b = (const char*)a.w_gate_up;
   f.dx.out = a.dx;
   f.dx.npan = (a.g.K + TB - 1) / TB;
-  f.dx.room = dx_room(a, n);
+  set_row_tiles(&f.dx, dx_room(a, n));
   f.gu = weight_tiles(gu_groups(a), a.d_pre, a.x, n > 1 ? part : a.dw_gate_up, n > 1 || a.dw32, n);
   f.down = weight_tiles(down_groups(a), a.dy, a.h, n > 1 ? down_part : a.dw_down, n > 1 || a.dw32, n);
   f.dx_units = a.g.rows > 0 ? (int)dx_units(a, n) : 0;

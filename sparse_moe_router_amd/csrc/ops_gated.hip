@@ -161,7 +161,7 @@ hipError_t launch_gated(const Groups& g, const void* x, const void* w, void* h, 
   t.a = (const char*)x;
   t.b = (const char*)w;
   t.npan = (g.N + GATED_COLS - 1) / GATED_COLS;
-  t.room = kChainGroups;
+  set_row_tiles(&t);
   const GatedEpi epi{(uint16_t*)h, g.ldy, (uint16_t*)pre, ldp};
   const dim3 gr((unsigned)gated_units(g)), bl(512);
   const Launch lc{s, nullptr, nullptr};
@@ -175,7 +175,7 @@ hipError_t launch_gated_grad(const Groups& g, const void* dy, const void* w, con
   t.a = (const char*)dy;
   t.b = (const char*)w;
   t.npan = (g.K + TB - 1) / TB;
-  t.room = kChainGroups;
+  set_row_tiles(&t);
   const GatedGradEpi epi{(const uint16_t*)pre, ldp, (uint16_t*)d_pre, ldd, (uint16_t*)h, ldh};
   return launch(Launch{s, nullptr, nullptr}, k_gated_grad, dim3((unsigned)op_tile_units(OP_NN, g)), dim3(512), t, epi);
 }

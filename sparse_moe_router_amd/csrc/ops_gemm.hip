@@ -86,7 +86,7 @@ hipError_t launch_op_tile(OpKind kind, bool i8, const Groups& g, const void* a, 
   t.fp32 = fp32;
   t.nrow = (g.N + TB - 1) / TB;
   t.npan = ((kind == OP_NT ? g.N : g.K) + TB - 1) / TB;
-  t.room = kChainGroups;
+  set_row_tiles(&t);
   const unsigned grid = (unsigned)op_tile_units(kind, g);
   const Launch lc{s, nullptr, nullptr};
   const bool far = rows_far(g, i8 ? 1 : 2);

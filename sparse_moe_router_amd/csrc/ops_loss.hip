@@ -456,7 +456,7 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t s) {
   t.a = (const char*)a.x;
   t.b = (const char*)a.w;
   t.npan = panels;
-  t.room = kChainGroups;
+  set_row_tiles(&t);
   const bool few = takes_matrix_vector_logits(a.rows, a.V);
   const hipError_t e = few ? launch_loss_skinny(t.g, a.x, a.w, tokens, false, s)
                            : launch_rows(lc, k_loss_logits<true>, k_loss_logits<false>, t, LseEpi{tokens, a.rows});
@@ -541,7 +541,7 @@ hipError_t launch_loss_grad(const LossArgs& a, void* workspace, hipStream_t s) {
     t.a = (const char*)a.x;
     t.b = w;
     t.npan = (n + TB - 1) / TB;
-    t.room = kChainGroups;
+    set_row_tiles(&t);
     hipError_t e = hipSuccess;
     if (a.rows > 0) {
       tokens.v0 = (int)v0;

@@ -27,7 +27,8 @@ struct TileArgs {
   int fp32;
   int npan;    // tiles along the second output dimension
   int nrow;    // TN: tiles along n
-  int room;    // NT, NN: workgroups that the tiles may take
+  int tiles, height;    // NT, NN, one group: number of row tiles, rows of each (set_row_tiles)
+  int shift;            // several groups: exponent of 2 of the height
   int splits;           // TN: parts of the reduction (0 and 1: the whole)
   const float* factor;  // ScaledEpi
 };
@@ -127,7 +128,7 @@ struct RowTile {
 // rows of int8 42 and 28 for 1000 x 4096 x 4096; 1000 x 2048 against 1000 columns of logits 46 and 26).
 // `room`: the workgroups that the tiles of all panels may take.
 // Of one group: the number of its tiles.
-__host__ __device__ inline int64_t dense_tiles(int64_t rows, int64_t npan, int room) {
+inline int64_t dense_tiles(int64_t rows, int64_t npan, int room) {
   for (int h = 64; h < TB; h += 64) {
     const int64_t n = (rows + h - 1) / h;
     if (n * npan <= room) return n;
@@ -135,32 +136,39 @@ __host__ __device__ inline int64_t dense_tiles(int64_t rows, int64_t npan, int r
   return (rows + TB - 1) / TB;
 }
 // Of several groups, whose sizes only the device knows: the exponent of 2 of the height.
-__host__ __device__ inline int64_t most_tiles(const Groups& g, int shift) {
+inline int64_t most_tiles(const Groups& g, int shift) {
   return (g.rows >> shift) + (g.E < g.rows ? g.E : g.rows);
 }
-__host__ __device__ inline int tile_shift(const Groups& g, int64_t npan, int room) {
+inline int tile_shift(const Groups& g, int64_t npan, int room) {
   return most_tiles(g, 6) * npan <= room ? 6 : most_tiles(g, 7) * npan <= room ? 7 : 8;
 }
 static_assert(TB == 1 << 8, "tile_shift");
+// The heights for the kernels, from g and npan (found by every workgroup, 8-bit products of 4096 x 4096 x 256 take
+// 18.9 us, not 18.3; rows' gradients of 32768 rows over 256 experts of 512 x 2048 162.8, not 161.6).
+inline void set_row_tiles(TileArgs* t, int room = kChainGroups) {
+  const int64_t n = dense_tiles(t->g.rows, t->npan, room);
+  t->tiles = (int)n;
+  // Where all units run at a time, the tiles share the rows evenly, in whole blocks of 32: the tallest one
+  // takes the time of the launch (257 rows against 32003 columns of 2048: 256 + 1 rows 56 us, 160 + 97 50).
+  t->height = n > 0 && n * t->npan <= kChainGroups ? (int)((t->g.rows + 32 * n - 1) / (32 * n)) * 32 : TB;
+  t->shift = tile_shift(t->g, t->npan, room);
+}
 
 // One group: the units (tile, panel) are cut into eight equal runs, one for
 // each XCD, and within a run into blocks of four tiles, panel by panel: the 32
 // workgroups that an XCD runs at a time then read about as many tiles' rows as
 // panels' weights (int8 4096 x 8192 x 4096: 126 -> 119 us).
-__device__ __forceinline__ RowTile find_tile_dense(const Groups& g, int xcd, int64_t local, int npan, bool aligned, int room) {
+__device__ __forceinline__ RowTile find_tile_dense(const TileArgs& p, int xcd, int local, bool aligned) {
   constexpr int SG = 4;
-  const int64_t total = dense_tiles(g.rows, npan, room);
-  // Where all units run at a time, the tiles share the rows evenly, in whole blocks of 32: the tallest one
-  // takes the time of the launch (257 rows against 32003 columns of 2048: 256 + 1 rows 56 us, 160 + 97 50).
-  const int height_rows = total * npan <= kChainGroups ? (int)((g.rows + 32 * total - 1) / (32 * total)) * 32 : TB;
-  const int64_t run = (total * npan + 7) / 8, unit = xcd * run + local;
+  const Groups& g = p.g;
+  const int total = p.tiles, npan = p.npan;  // at most kOpMaxUnits units
+  const int run = (total * npan + 7) / 8, unit = xcd * run + local;
   if (local >= run || unit >= total * npan) return RowTile{-1, 0, 0, 0, 0};
-  const int64_t sg = unit / (SG * npan), sr = unit - sg * SG * npan;
-  const int64_t height = total - sg * SG < SG ? total - sg * SG : SG;
-  const int64_t p0 = (sg * SG + sr % height) * height_rows;
+  const int sg = unit / (SG * npan), sr = unit - sg * SG * npan;
+  const int height = total - sg * SG < SG ? total - sg * SG : SG, panel = sr / height;
+  const int64_t p0 = (int64_t)(sg * SG + sr - panel * height) * p.height;
   if (p0 >= g.rows) return RowTile{-1, 0, 0, 0, 0};
-  return RowTile{0, p0, (int)(g.rows - p0 < height_rows ? g.rows - p0 : height_rows), (int)(sr / height),
-                 total == 1 && aligned};
+  return RowTile{0, p0, (int)(g.rows - p0 < p.height ? g.rows - p0 : p.height), panel, total == 1 && aligned};
 }
 
 // Groups: the tiles in three classes, the tallest first, so that the short
@@ -183,9 +191,10 @@ __device__ __forceinline__ void four_ranges(const Groups& g, int e, int end, Ran
   for (int u = 0; u < 4; ++u) r[u] = limited(g, v[u], v[u + 1]);
 }
 __device__ __forceinline__ int tile_class(int rest) { return rest > 192 ? 0 : rest > 64 ? 1 : 2; }
-__device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t local, int npan, bool aligned, int room) {
-  if (!g.offsets) return find_tile_dense(g, xcd, local, npan, aligned, room);
-  const int shift = tile_shift(g, npan, room), low = (1 << shift) - 1;
+__device__ __forceinline__ RowTile find_tile(const TileArgs& p, int xcd, int local, bool aligned) {
+  if (!p.g.offsets) return find_tile_dense(p, xcd, local, aligned);
+  const Groups& g = p.g;
+  const int npan = p.npan, shift = p.shift, low = (1 << shift) - 1;
   const int lane = threadIdx.x & 63, per = (g.E + 63) / 64;
   // tiles of this lane's groups in each class: bits 0..31, 32..47, 48..63
   uint64_t mine = 0;
@@ -212,7 +221,7 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
   int cl, panel;
   if (total >= kDealTiles) {
     i = local / npan;
-    panel = (int)(local % npan);
+    panel = local % npan;
     const int64_t a0 = n0 * xcd / 8, m0 = n0 * (xcd + 1) / 8 - a0;
     const int64_t a1 = n1 * xcd / 8, m1 = n1 * (xcd + 1) / 8 - a1;
     const int64_t a2 = n2 * xcd / 8, m2 = n2 * (xcd + 1) / 8 - a2;
@@ -227,7 +236,7 @@ __device__ __forceinline__ RowTile find_tile(const Groups& g, int xcd, int64_t l
     }
   } else {
     i = (local * 8 + xcd) / npan;
-    panel = (int)((local * 8 + xcd) % npan);
+    panel = (local * 8 + xcd) % npan;
     if (i >= total) return RowTile{-1, 0, 0, 0, 0};
     cl = i < n0 ? 0 : i < n0 + n1 ? 1 : 2;
     i -= cl == 0 ? 0 : cl == 1 ? n0 : n0 + n1;
@@ -820,7 +829,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& p, TileJob job, u32
 // rows again.
 template <OpKind KIND, bool I8, int GX, class EPI = StoreEpi>
 __device__ __forceinline__ void row_tile(const TileArgs& p, u32x4_t* lds, const EPI& epi = EPI{}) {
-  RowTile tl = find_tile(p.g, blockIdx.x & 7, blockIdx.x >> 3, p.npan, p.g.K * (I8 ? 1 : 2) % 128 == 0, p.room);
+  RowTile tl = find_tile(p, blockIdx.x & 7, blockIdx.x >> 3, p.g.K * (I8 ? 1 : 2) % 128 == 0);
   // the same in every lane, which the compiler cannot see behind the scan
   tl = RowTile{__builtin_amdgcn_readfirstlane(tl.e), uniform64(tl.p0), __builtin_amdgcn_readfirstlane(tl.rows),
                __builtin_amdgcn_readfirstlane(tl.panel), __builtin_amdgcn_readfirstlane(tl.once)};
@@ -855,9 +864,9 @@ __device__ __forceinline__ void row_tile(const TileArgs& p, u32x4_t* lds, const 
 // whole ones.
 template <OpKind KIND, class EPI = StoreEpi>
 __device__ __forceinline__ void row_chain(const TileArgs& p, u32x4_t* lds, const EPI& epi = EPI{}) {
-  int64_t local = blockIdx.x >> 3;
+  int local = blockIdx.x >> 3;
   auto take = [&](TileJob* t) __attribute__((always_inline)) {
-    const RowTile tl = find_tile_dense(p.g, blockIdx.x & 7, local, p.npan, false, p.room);
+    const RowTile tl = find_tile_dense(p, blockIdx.x & 7, local, false);
     *t = TileJob{0, tl.p0, tl.rows, 0, 0, tl.panel};
     return tl.e >= 0;
   };
