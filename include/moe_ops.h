@@ -78,7 +78,7 @@ moe_status_t moe_grouped_matmul(const moe_groups_t* g, const void* x, const void
 /* dx[p][k] = sum_n dy[p][n] w[e][n][k]: the gradient of the grouped rows (of
  * the copies that row(p) took: a token's own gradient is the sum over its
  * assignments).  dy bf16 [rows][ldy], w as above, dx bf16 or fp32
- * [rows][ldx].  perm, top_k and x_rows are not used. */
+ * [rows][ldx].  perm, top_k and x_rows are not used, but have to be within their ranges. */
 moe_status_t moe_grouped_matmul_grad_input(const moe_groups_t* g, const void* dy, const void* w, void* dx,
                                            moe_dtype_t dx_type, hipStream_t stream);
 
@@ -202,7 +202,7 @@ moe_status_t moe_gated_matmul(const moe_groups_t* g, const void* x, const void* 
  *   w          bf16 [E][N][K]
  *   gate_up, d_gate_up  bf16 [rows][ld] of 2 K columns
  *   h          bf16 [rows][ldx]
- * perm, top_k and x_rows are not used. */
+ * perm, top_k and x_rows are not used, but have to be within their ranges. */
 moe_status_t moe_gated_matmul_grad(const moe_groups_t* g, const void* dy, const void* w, moe_mat_t gate_up,
                                    moe_mat_t d_gate_up, void* h, hipStream_t stream);
 
@@ -225,8 +225,11 @@ typedef struct {
  * dy bf16 [rows][ld_dy], x bf16 [x_rows][ldx], w_gate_up bf16 [E][2 I][K], w_down bf16
  * [E][H][I], gate_up bf16 [rows][ld] of 2 I columns as the forward call kept it, dx bf16
  * [rows][ld], dw_gate_up and dw_down in dw_type, of the weights' shapes.  workspace:
- * moe_feed_forward_grad_workspace_size bytes, which hold d_gate_up, h (both bf16, or fp32 in
- * calls of few rows) and, where few experts have long groups, parts of the weight gradients. */
+ * moe_feed_forward_grad_workspace_size bytes, which hold d_gate_up, h and, where few experts have
+ * long groups, parts of the weight gradients.  d_gate_up and h are operands of the matrix units
+ * and so rounded to bf16, as where they are tensors between calls: the gradients are off by 0.17%
+ * of their norm before their own rounding, another 0.17% in bf16 (both: 0.23%).  Calls of at most
+ * 32 rows in which rows times weights, and experts times weights, are at most 2^28 keep them in fp32. */
 size_t moe_feed_forward_grad_workspace_size(const moe_feed_forward_t* d);
 moe_status_t moe_feed_forward_grad(const moe_feed_forward_t* d, const void* dy, const void* x, const void* w_gate_up,
                                    const void* w_down, moe_mat_t gate_up, moe_mat_t dx, void* dw_gate_up, void* dw_down,
@@ -327,8 +330,9 @@ moe_status_t moe_cross_entropy(const moe_loss_t* d, const void* x, const void* w
  * of largest magnitude of the tokens that have a target and r[t] = x[t] d_loss[t] / m, rounded to bf16.  lse as the forward call
  * gave it, d_loss fp32 [rows]; dx bf16 or fp32 [rows][ld] or not given, dw bf16 or
  * fp32 [V][H] or NULL.  The vocabulary goes by in pieces; the workspace
- * (moe_cross_entropy_grad_workspace_size bytes) holds one piece's dz, the sums of
- * dx and r.  Either gradient is the same, bit for bit, with and without the other. */
+ * (moe_cross_entropy_grad_workspace_size bytes) holds one piece's dz (at most 256 MB, or 4 KB a
+ * token above 65536 tokens), one to 32 sums of dx in fp32, r, and where a vocabulary is small
+ * parts of dw.  Either gradient is the same, bit for bit, with and without the other. */
 size_t moe_cross_entropy_grad_workspace_size(const moe_loss_t* d);
 moe_status_t moe_cross_entropy_grad(const moe_loss_t* d, const float* d_loss, const void* x, const void* w,
                                     const int64_t* target, const float* lse, moe_mat_t dx, moe_dtype_t dx_type, void* dw,

@@ -45,10 +45,11 @@ __device__ __forceinline__ u32x4_t pack(const float (&f)[8]) {
   return u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
 }
 
-// A thread takes eight columns of a token's row; rows of less than 2048 elements share a workgroup (WIDE:
-// they do not, and the token's indexes and weights come by scalar loads: 4096 x 8 rows of 2048 36.2 ->
-// 31.4 us, 4.8 TB/s).  Eight grouped rows are in flight
-// at a time.
+// A thread takes eight columns of a token's row; rows of up to 1024 elements share a workgroup (WIDE, from
+// 2048 on: one row, and the token's indexes and weights come by scalar loads: 4096 x 8 rows of 2048 36.2 ->
+// 31.4 us, 4.8 TB/s).  Between the two a workgroup has one row and threads without columns.  4096 x 8 rows, other
+// ones in each call but in part still cached: of 1024 elements 5.0 TB/s, 1032 3.6, 1536 5.0, 2040 4.5, 2048 5.6, 2056
+// 5.3.  Eight grouped rows are in flight at a time.
 template <class T>
 __device__ __forceinline__ T read_uniform(const T* p, int64_t i) {
   return ((const __attribute__((address_space(4))) T*)p)[i];

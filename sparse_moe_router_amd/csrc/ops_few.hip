@@ -10,8 +10,10 @@
 // d and h stay fp32 between the two launches: with few rows their roundings
 // would not average out.
 //
-// One row and one expert of 512 x 2048: 15.6 us (tiles 40); 8 rows over 8 experts of 1024 x 2048: 44 (68); 22 x 2
-// over 182 of 1016 x 400, most of them without rows: the gradients' 444 MB.
+// One row and one expert of 512 x 2048: 15.6 us (tiles 40); in a trace k_few_gate 9.2, four workgroups of which each goes
+// through 2048 rows of 256 bytes, and k_few_products 7.1.  8 rows over 8 experts of 1024 x 2048: 44 us (68), in a trace
+// 14.1 + 34.2; 32 rows 14.6 + 46.7, all of them of one expert 14.2 + 47.7.  22 x 2 over 182 of 1016 x 400, most of them
+// without rows: the gradients' 444 MB.
 #include "ops_internal.h"
 
 namespace moe {

@@ -58,7 +58,12 @@ inline bool quantizes_inside(int64_t rows, int64_t x_rows, int E, int N, int K) 
 // 12.0 / 12.4, 18.6 / 22.1 and 27.9 / 35.1; 400 tokens, 1000 columns (441) 11.8 /
 // 10.0, 14.4 / 12.4, 28.2 / 22.2 and 48.1 / 35.9; 1000 tokens, 1000 columns (1008)
 // 19.5 / 10.2, 23.2 / 12.6, 51.3 / 22.4 and 90.6 / 35.8; 16 tokens, 16000 columns
-// (1000) 12.9 / 10.1, 15.1 / 13.9, 26.5 / 31.1 and 43.7 / 53.1.
+// (1000) 12.9 / 10.1, 15.1 / 13.9, 26.5 / 31.1 and 43.7 / 53.1.  Beyond that the tiles lose up to a third to
+// 1 to 16 tokens of 16000 columns, and nothing from 32000 on, where their 125 and more workgroups share the
+// weights' stream: rows of 1024, 2048 and 4096 elements, 1 token x 16000 columns 15.8 / 18.3, 21.1 / 29.3 and
+// 34.0 / 49.8; x 32000 26.1 / 20.1, 37.2 / 35.9 and 62.5 / 63.9, 16 tokens 33.0 / 20.0, 47.7 / 36.2 and 82.5 /
+// 64.9; 1 token x 64000 47.1 / 28.5, 68.7 / 66.5 and 119.6 / 105.2; x 128000 88.2 / 52.8, 132 / 113 and 233 /
+// 204, 16 tokens 116 / 52.7, 175 / 116 and 310 / 207.
 constexpr int64_t kSkinnyLogitGroups = 256;
 inline bool takes_matrix_vector_logits(int64_t rows, int64_t columns) {
   return (rows + 63) / 64 * ((columns + 15) / 16) <= kSkinnyLogitGroups;
@@ -71,7 +76,12 @@ inline bool takes_matrix_vector_logits(int64_t rows, int64_t columns) {
 // 34 / 42, 55 / 44; 1 of 2048 x 4096 47 / 103, 58 / 104, 80 / 106, 144 / 110; 4 of 584 x 1456 19.9 / 39.1, 21.8
 // / 38.3, 26 / 39, 35 / 39, 58 / 40; 8 of 88 x 376 8.2 / 17.8, 8.8 / 18.2, 9.5 / 18.1, 11.4 / 17.9, 15.1 / 18.8;
 // 16 of 1408 x 4096 135 / 159, 192 / 195, 230 / 211, 311 / 230; 64 of 512 x 2048 90 / 97, 103 / 113, 118 / 121,
-// 139 / 136; 256 of 512 x 2048 287 / 287, 302 / 291, 319 / 298, 351 / 332.
+// 139 / 136; 256 of 512 x 2048 287 / 287, 302 / 291, 319 / 298, 351 / 332; 8 of 1024 x 2048 35 / 70, 57 / 69, 61 /
+// 69, 75 / 69.  With all rows on one of the experts, 8, 16 and 32 rows: 8 of 1024 x 2048 40 / 70, 47 / 71, 60 / 74;
+// 64 of 512 x 2048 93 / 98, 99 / 101, 110 / 103; 64 of 128 x 512 17 / 23, 21 / 24, 28 / 25; 8 of 88 x 376 11.8 / 18.2,
+// 15.5 / 18.8, 23.1 / 19.8 (a weight gradient's workgroup walks its expert's rows one after another).  The bounds
+// are round ones: at their edges either side loses up to a fifth (16 rows of 2048 x 4096 take tiles at 106 for 80,
+// 1 row over 16 of 1408 x 4096 at 160 for 135; 32 rows over 64 experts the few-row kernels at 145 for 133).
 constexpr int64_t kFewRows = 32, kFewRead = 1 << 28, kFewWritten = 1 << 28;
 inline bool takes_few_rows(int64_t rows, int64_t E, int64_t H, int64_t I, int64_t K) {
   const int64_t weights = I * (2 * K + H);
@@ -85,8 +95,10 @@ constexpr int kChainGroups = 256;
 // time.  launch_steps: the time, in steps of 64, of a launch of n0 tiles of s0 steps and then n1 tiles of s1,
 // each started where one before it ends.  A tile costs kTileSteps beside its own steps, a launch behind it
 // kLaunchSteps, and kStepBytes of fp32 parts written or read one.  (Fitted to 450 timings of cross
-// entropies' and feed-forward blocks' gradients at 1 to 32 slices and parts: over 27 problems the choices cost
-// 0.6% more than the best ones, those of a rule that filled the workgroups 7%.)
+// entropies' and feed-forward blocks' gradients at 1 to 32 slices and parts.  Over 8 blocks the choices are the
+// best ones timed; over 19 cross entropies they cost 1.1% more with both gradients and 2.8% for dx alone, which
+// a choice weighs a third of both: at worst 18%, 92 for 78 us, for the dx of 2000 tokens against 4000 x 1024.
+// Those of a rule that filled the workgroups cost 7%.)
 constexpr int kTileSteps = 7, kLaunchSteps = 2;
 constexpr int64_t kStepBytes = 4 << 20;
 constexpr int64_t kMostTiles = 2 * kChainGroups;  // of a cut reduction: more cost more

@@ -125,7 +125,12 @@ struct RowTile {
 // Heights of row tiles: where all of them run at a time, low ones, each of which takes less (a tile takes 0.6
 // us a step of up to 64 rows, 1 of 128 and 1.45 of 256; measured, us, tiles of 256 and these: 2000 x 2048 x
 // 2048 40 and 26, 256 x 8192 x 1024 25 and 16, 8192 x 512 x 4096 67 and 43, 400 x 1024 x 4096 66 and 34, by
-// rows of int8 42 and 28 for 1000 x 4096 x 4096; 1000 x 2048 against 1000 columns of logits 46 and 26).
+// rows of int8 42 and 28 for 1000 x 4096 x 4096; 1000 x 2048 against 1000 columns of logits 46 and 26).  Of
+// several groups, forward products of rows x N x K: 1024 x 4096 x 4096 over 2 67 and 44, 700 x 4096 x 2048 over 2
+// 38 and 22, 2000 x 512 x 1024 over 8 23.8 and 13.4, 600 x 1536 x 2048 over 8 33 and 25, 4000 x 256 x 512 over 4
+// 16.0 and 9.3; where the weights' stream bounds both, and two to four low tiles of a group read its weights: 512 x
+// 4096 x 4096 over 8 67 and 62 with skewed groups, 70 and 67 with even ones, 512 x 2048 x 4096 over 8 skewed 68 and
+// 54, 512 x 8192 x 2048 over 4 44 and 42.
 // `room`: the workgroups that the tiles of all panels may take.
 // Of one group: the number of its tiles.
 inline int64_t dense_tiles(int64_t rows, int64_t npan, int room) {

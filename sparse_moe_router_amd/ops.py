@@ -335,7 +335,8 @@ def feed_forward_grad(dy: torch.Tensor, x: torch.Tensor, w_gate_up: torch.Tensor
     """moe_feed_forward_grad: the gradients of :func:`feed_forward` from dy (bf16 [rows, H]) and the gate_up
     that it saved, as a dict: ``x`` (bf16, of each grouped row: :func:`combine` with top_k sums a
     token's), ``w_gate_up`` and ``w_down`` (in dw_dtype; zeros for an expert without rows).  The
-    gradient of gate_up and h are rounded to bf16 between the kernels, except in calls of few rows."""
+    gradient of gate_up and h are rounded to bf16 between the kernels, except in calls of few rows
+    (include/moe_ops.h has the sizes and the errors)."""
     return _call(stream, _ops.feed_forward_grad, dy, x, w_gate_up, w_down, gate_up, offsets, perm, top_k,
                  _fp32(dw_dtype), workspace)
 
